@@ -464,6 +464,120 @@ pkv_status pkv_paged_attention_decode_static_ws(const pkv_cache_desc* cache,
                                                 void* out, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The 8-bit cache with a scale per block and KV head (the pages name the 8-bit
+ * float cache, 「KV 缓存与分页注意力」 §11; how it is scaled is this library's
+ * choice).  A "scaled cache" is a pkv_cache_desc of PKV_FP8_E4M3, whose k_scale
+ * and v_scale are then not used, with one array of scales per layer beside it:
+ *   scales   device float [num_blocks][num_kv_heads][2], 8-byte aligned:
+ *            the scale of K and of V.  A value is its code times its scale.
+ * The calls that take `scales` form one path: pkv_rope_append writes codes and
+ * scales, pkv_paged_attention_decode_scaled and _prefill_scaled read them, and
+ * pkv_copy_blocks_scaled copies or swaps blocks with them.  The calls above
+ * read such a cache as one with a single scale, which is not what it holds.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * rope_append -- rotary positions on the new tokens' q and K, and the append of
+ * K and V, for the batch layout of pkv_paged_attention_prefill: sequence s has
+ * the rows [cu_seqlens_q[s], cu_seqlens_q[s + 1]), which are the last n_s
+ * tokens of its context_lens[s] (a decode step: n_s = 1).
+ *
+ * Row j of sequence s has position p = context_lens[s] - n_s + j.  With
+ * (cos, sin) of p * inv_freq[i], pair i of every head of q and K becomes
+ *   a' = mscale (a cos - b sin),  b' = mscale (b cos + a sin);
+ * pair i is elements (i, i + rot_dim / 2), or (2i, 2i + 1) when `interleaved`;
+ * elements from rot_dim on stay as they are.  Angles are exact to 2^-20 turns
+ * far past 2^24 tokens; arithmetic is fp32, rounded once to what is written.
+ *
+ * cache, scales  scales NULL: the cache as pkv_kv_append takes it (in_dtype, or
+ *                E4M3 with k_scale / v_scale).  Otherwise a scaled cache:
+ *                bound = max(1, sqrt2 |mscale|) max|K| before the rotation, or
+ *                max|V|, over the finite elements that the call writes into
+ *                the block for that head, and need = the smallest power of two
+ *                s >= 2^-126 with bound <= 448 s.  A block whose first slot
+ *                the call writes gets scale = need; any other block keeps the
+ *                larger of its scale and need, and when that is larger than
+ *                it was, the codes of its earlier tokens become
+ *                E4M3(code * old / new).  New codes are E4M3(x / scale), to
+ *                nearest even; infinities saturate, NaN stays NaN.
+ * q, k, v        device [total_q][num_heads or num_kv_heads][head_dim] of
+ *                in_dtype; q_stride, k_stride, v_stride: elements between
+ *                tokens (a multiple of 8; slices of one projection's output
+ *                will do).  q may be NULL: K and V alone.
+ * inv_freq       device double [rot_dim / 2], radians per position, below 2^52
+ *                (position interpolation of any kind is in these).
+ * rot_dim        a multiple of 16 up to head_dim; 0 rotates nothing.
+ * q_out          device [total_q][num_heads][head_dim], dense; may be q itself
+ *                when q is dense.
+ * block_tables, max_blocks_per_seq, context_lens, max_context_len, max_q_len
+ *                as for the prefill.  Blocks that the call writes must not be
+ *                shared with another sequence (copy them first).
+ * Rows of q_out that belong to no sequence are left as they were.
+ * Device checks (with dev_err): n_s above max_q_len or c, c above
+ *   max_context_len or the table, bad cu_seqlens_q -> PKV_DEVERR_CONTEXT,
+ *   nothing of that sequence is written; a bad block id -> PKV_DEVERR_BLOCK_ID,
+ *   its K and V are skipped.
+ * Launches: one kernel.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, int32_t in_dtype, int32_t num_heads,
+                           const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                           float mscale, int32_t num_seqs, const int32_t* cu_seqlens_q,
+                           int32_t total_q, int32_t max_q_len, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t max_context_len, int32_t* dev_err, void* q_out,
+                           pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode attention over a scaled cache: pkv_paged_attention_decode with k_t and
+ * v_t = code * scale of their block and KV head.  q and out F16 or BF16, 1..16
+ * query heads per KV head; partition_size a multiple of block_size and of 16,
+ * or 0.  The workspace has the layout given above, of
+ * pkv_decode_scaled_workspace_bytes(...) bytes for the partition size of
+ * pkv_decode_scaled_partition_size(...).  A block with a bad id contributes
+ * nothing.  The same inputs and partition size give the same bits.
+ * Scales are positive and finite; V's small next to the largest of the context
+ * lose no precision down to a ratio of 2^-20.
+ * ------------------------------------------------------------------------- */
+int32_t pkv_decode_scaled_partition_size(const pkv_cache_desc* cache, int32_t num_seqs,
+                                         int32_t num_heads, int32_t max_context_len,
+                                         int32_t requested);
+
+size_t pkv_decode_scaled_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                         int32_t num_heads, int32_t max_context_len,
+                                         int32_t partition_size);
+
+pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const float* scales,
+                                             const void* q, int32_t q_dtype, int32_t num_seqs,
+                                             int32_t num_heads, const int32_t* block_tables,
+                                             int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, int32_t max_context_len,
+                                             float scale, int32_t partition_size,
+                                             void* workspace, size_t workspace_bytes,
+                                             int32_t* dev_err, void* out, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Copy of whole blocks with their scales, every layer: pkv_copy_blocks
+ * (copy-on-write) inside one pool when dst is NULL, pkv_swap_blocks between two
+ * pools otherwise (either may be pinned, device-mapped host memory; every
+ * pointer is then checked).
+ *
+ * src, dst                host arrays of num_layers scaled-cache descriptors.
+ * src_scales, dst_scales  host arrays of num_layers scale arrays.
+ * block_pairs             int64 [num_pairs][2] (src block, dst block), device
+ *                         memory (or pinned host memory when dst is given).
+ * A pair outside its pool is skipped and flags PKV_DEVERR_COPY_PAIR.
+ * Precondition (not checked): dst blocks are distinct, and no dst is also a src
+ * of the same pool.
+ * Launches: one kernel per 64 layers and 65,535 pairs.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_copy_blocks_scaled(const pkv_cache_desc* src, float* const* src_scales,
+                                  const pkv_cache_desc* dst, float* const* dst_scales,
+                                  int32_t num_layers, const int64_t* block_pairs,
+                                  int64_t num_pairs, int32_t* dev_err, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * pkv_testing_set_decode_wait_limit -- a testing aid, not part of the method
  * (the pages have no counterpart).
  *

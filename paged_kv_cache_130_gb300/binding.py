@@ -82,6 +82,14 @@ def load():
         "pkv_paged_attention_decode_shared_prefix": (i32, [dp, vp, i32, i32, i32, vp, i32, vp,
                                                            i32, i32, vp, vp, i32, i32, f32, i32,
                                                            vp, ctypes.c_size_t, vp, vp, vp]),
+        "pkv_rope_append": (i32, [dp, vp, vp, i64, vp, i64, vp, i64, i32, i32, vp, i32, i32, f32,
+                                  i32, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp]),
+        "pkv_decode_scaled_partition_size": (i32, [dp, i32, i32, i32, i32]),
+        "pkv_decode_scaled_workspace_bytes": (ctypes.c_size_t, [dp, i32, i32, i32, i32]),
+        "pkv_paged_attention_decode_scaled": (i32, [dp, vp, vp, i32, i32, i32, vp, i32, vp, i32,
+                                                    f32, i32, vp, ctypes.c_size_t, vp, vp, vp]),
+        "pkv_copy_blocks_scaled": (i32, [dp, ctypes.POINTER(vp), dp, ctypes.POINTER(vp), i32, vp,
+                                         i64, vp, vp]),
         "pkv_testing_set_decode_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),
         "pkv_testing_set_shared_prefix_path": (i32, [i32]),
         "pkv_testing_stream_copy": (i32, [vp, vp, i64, vp]),
@@ -399,3 +407,133 @@ def pkv_block_hashes(token_ids, cu_seqlens, block_size, block_offsets=None, pare
                                    _stream(stream)), "pkv_block_hashes")
     return hashes[:total_blocks]
 
+
+# ------------------------------------------------------------------ scaled cache
+
+def _i32(t, name):
+    _dense(t, name)
+    if t.dtype != torch.int32:
+        raise ValueError("%s must be int32" % name)
+    return t
+
+
+def _scales_of(cache, scales):
+    """Device address of a layer's scales, float32 [num_blocks, num_kv_heads, 2]."""
+    _dense(scales, "scales")
+    if scales.dtype != torch.float32 or scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads:
+        raise ValueError("scales must be float32 [num_blocks, num_kv_heads, 2]")
+    return scales.data_ptr()
+
+
+def _token_rows(t, name, dtype=None, heads=None, dim=None, rows=None):
+    """Elements between the tokens of t [rows, heads, head_dim], whose heads lie
+    side by side (a slice of a fused projection will do)."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("%s must be [tokens, heads, head_dim] with dense heads" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("q, k and v must have the same type")
+    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim) or \
+            (rows is not None and t.shape[0] != rows):
+        raise ValueError("%s does not fit the cache or the other inputs" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tables, context_lens,
+                    max_context_len, interleaved=False, mscale=1.0, scales=None, dev_err=None,
+                    q_out=None, stream=None):
+    """Rotate q and K by their positions and append K and V; returns the rotated
+    q (None without q).  `inv_freq` is a float64 device tensor of rot_dim / 2
+    radians per position (rope.inv_freq computes it), or None to rotate
+    nothing; with `scales` the cache is a scaled one."""
+    rows = k.shape[0]
+    ks = _token_rows(k, "k", heads=cache.num_kv_heads, dim=cache.head_dim)
+    vs = _token_rows(v, "v", k.dtype, cache.num_kv_heads, cache.head_dim, rows)
+    qs, heads = 0, 0
+    if q is not None:
+        qs, heads = _token_rows(q, "q", k.dtype, dim=cache.head_dim, rows=rows), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+            raise ValueError("q_out must be dense and like q")
+    rot = 0
+    if inv_freq is not None:
+        _dense(inv_freq, "inv_freq")
+        if inv_freq.dtype != torch.float64:
+            raise ValueError("inv_freq must be float64")
+        rot = 2 * inv_freq.numel()
+    num_seqs = context_lens.numel()
+    if cu_seqlens_q.numel() != num_seqs + 1:
+        raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
+    _check(load().pkv_rope_append(
+        ctypes.byref(cache), _scales_of(cache, scales) if scales is not None else None,
+        q.data_ptr() if q is not None else None, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        dtype_code(k.dtype), heads, inv_freq.data_ptr() if rot else None, rot,
+        1 if interleaved else 0, mscale, num_seqs, _i32(cu_seqlens_q, "cu_seqlens_q").data_ptr(),
+        rows, max_q_len, _i32(block_tables, "block_tables").data_ptr(), block_tables.shape[1],
+        _i32(context_lens, "context_lens").data_ptr(), max_context_len, _ptr(dev_err),
+        q_out.data_ptr() if q is not None else None, _stream(stream)), "pkv_rope_append")
+    return q_out if q is not None else None
+
+
+def pkv_decode_scaled_partition_size(cache, num_seqs, num_heads, max_context_len, requested=0):
+    return int(load().pkv_decode_scaled_partition_size(ctypes.byref(cache), num_seqs, num_heads,
+                                                       max_context_len, requested))
+
+
+def pkv_decode_scaled_workspace_bytes(cache, num_seqs, num_heads, max_context_len,
+                                      partition_size=0):
+    return int(load().pkv_decode_scaled_workspace_bytes(ctypes.byref(cache), num_seqs, num_heads,
+                                                        max_context_len, partition_size))
+
+
+def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_lens,
+                                      max_context_len, scale, partition_size=0, workspace=None,
+                                      dev_err=None, out=None, stream=None):
+    """Decode over a scaled cache; arguments as pkv_paged_attention_decode."""
+    _dense(q, "q")
+    s, h, d = q.shape
+    if d != cache.head_dim or context_lens.numel() != s or block_tables.shape[0] != s:
+        raise ValueError("q, block_tables and context_lens do not fit together")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be dense and like q")
+    if workspace is None:
+        need = pkv_decode_scaled_workspace_bytes(cache, s, h, max_context_len, partition_size)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(load().pkv_paged_attention_decode_scaled(
+        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), dtype_code(q.dtype), s, h,
+        _i32(block_tables, "block_tables").data_ptr(), block_tables.shape[1],
+        _i32(context_lens, "context_lens").data_ptr(), max_context_len, scale, partition_size,
+        _ptr(workspace), ws_bytes, _ptr(dev_err), out.data_ptr(), _stream(stream)),
+        "pkv_paged_attention_decode_scaled")
+    return out
+
+
+def pkv_copy_blocks_scaled(caches, scales, block_pairs, dst=None, dst_scales=None, dev_err=None,
+                           stream=None):
+    """Copy blocks with their scales: inside one pool, or with `dst` and
+    `dst_scales` from one pool to another (device or pinned host memory)."""
+    if isinstance(caches, CacheDesc):
+        caches, scales = [caches], [scales]
+        if dst is not None:
+            dst, dst_scales = [dst], [dst_scales]
+    n = len(caches)
+    if len(scales) != n or (dst is None) != (dst_scales is None) or \
+            (dst is not None and (len(dst) != n or len(dst_scales) != n)):
+        raise ValueError("one array of scales per layer, and as many layers on both sides")
+    _dense(block_pairs, "block_pairs")
+    if block_pairs.dtype != torch.int64:
+        raise ValueError("block_pairs must be int64 [n, 2]")
+    ptrs = ctypes.c_void_p * n
+    a = (CacheDesc * n)(*caches)
+    a_s = ptrs(*[_scales_of(c, t) for c, t in zip(caches, scales)])
+    b = b_s = None
+    if dst is not None:
+        b = (CacheDesc * n)(*dst)
+        b_s = ptrs(*[_scales_of(c, t) for c, t in zip(dst, dst_scales)])
+    _check(load().pkv_copy_blocks_scaled(a, a_s, b, b_s, n, _ptr(block_pairs),
+                                         block_pairs.numel() // 2, _ptr(dev_err),
+                                         _stream(stream)), "pkv_copy_blocks_scaled")

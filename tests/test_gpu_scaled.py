@@ -1,0 +1,419 @@
+"""The scaled 8-bit cache (a power-of-two scale per block and KV head) and the
+rotary append against the 64-bit oracle (oracle/scaled.py).
+
+Bounds, from the arithmetic:
+* rotated values: the fp32 cosine and sine are off by at most 2^-21 (a half
+  turn's fraction rounded to 24 bits gives pi 2^-25, sincospi itself 2^-22), the
+  two products and the sum by 2^-23 of |a| + |b|; e = 2^-20 m (|a| + |b|) covers
+  both.  Then one rounding: half a step of the 16-bit type, or of E4M3 (2^-4 of
+  the code, half a subnormal step 2^-10) times the scale.
+* scales, V's codes, and K's codes without a rotation: exact.
+* attention: 2e-3 + 2e-3 |ref|, plus half a bf16 step (harness): the weights are
+  rounded to fp16 (2^-12 each), scores carry fp32 sums of exact products.
+Unwritten slots hold 0xFF (NaN codes) and unused scales NaN, so that a read of
+either shows.
+"""
+import numpy as np
+import pytest
+import torch
+
+import harness as H
+import oracle
+from oracle import scaled as OS
+from paged_kv_cache_130_gb300 import binding as B
+from paged_kv_cache_130_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    H.build_library()
+
+
+TD = {W.F16: torch.float16, W.BF16: torch.bfloat16}
+
+
+class Batch:
+    """Sequences with `new` tokens after `cached` ones over a scattered pool.
+    Host copies (codes, scales) evolve through the oracle, device ones through
+    the library; both start from the same cached tokens."""
+
+    def __init__(self, seed, dt, heads, kv, d, bs, new, cached, size=1.0, spread=0.0, fill=True):
+        r = self.r = np.random.default_rng(seed)
+        self.dt, self.heads, self.kv, self.d, self.bs = dt, heads, kv, d, bs
+        self.new, self.cached = np.asarray(new), np.asarray(cached)
+        self.ctx = (self.new + self.cached).astype(np.int32)
+        self.cu = np.concatenate([[0], np.cumsum(self.new)]).astype(np.int32)
+        counts = -(-self.ctx // bs)
+        self.nb = int(counts.sum()) + 5
+        order = r.permutation(self.nb).astype(np.int32)
+        self.tables = np.full((len(self.ctx), max(1, int(counts.max()))), -1, np.int32)
+        at = 0
+        for i, n in enumerate(counts):
+            self.tables[i, :n] = order[at:at + n]
+            at += n
+        shape = (self.nb, kv, bs, d)
+        self.k, self.v = np.full(shape, 0xff, np.uint8), np.full(shape, 0xff, np.uint8)
+        self.scales = np.full((self.nb, kv, 2), np.nan, np.float32)
+        self.size, self.spread = size, spread
+        if fill and self.cached.sum():
+            n = int(self.cached.sum())
+            cu = np.concatenate([[0], np.cumsum(self.cached)])
+            for w, c in ((0, self.k), (1, self.v)):
+                x = self.values(n, kv)
+                OS.append_scaled(c, self.scales, w, x, x, 1.0, cu, self.tables, self.cached)
+        rows = int(self.cu[-1])
+        self.q = self.values(rows, heads, 1.0, 0.0)
+        self.nk, self.nv = self.values(rows, kv), self.values(rows, kv)
+        self.upload()
+
+    def values(self, rows, heads, size=None, spread=None):
+        size, spread = (self.size if size is None else size), (self.spread if spread is None else spread)
+        x = self.r.standard_normal((rows, heads, self.d)) * size
+        x = x * np.exp2(np.round(spread * self.r.standard_normal((rows, heads, 1))))
+        return torch.from_numpy(x).to(TD[self.dt]).double().numpy()
+
+    def dev16(self, x):
+        return torch.from_numpy(np.ascontiguousarray(x)).to(TD[self.dt]).cuda()
+
+    def upload(self):
+        self.gk, self.gv = torch.from_numpy(self.k.copy()).cuda(), torch.from_numpy(self.v.copy()).cuda()
+        self.gs = torch.from_numpy(self.scales.copy()).cuda()
+        self.desc = B.cache_desc(self.gk, self.gv)
+        self.gt, self.gctx = torch.from_numpy(self.tables).cuda(), torch.from_numpy(self.ctx).cuda()
+        self.gcu = torch.from_numpy(self.cu).cuda()
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.max_ctx, self.max_new = int(self.ctx.max()), int(self.new.max())
+
+    def append(self, inv_freq=None, interleaved=False, mscale=1.0, q=None, k=None, v=None, **kw):
+        f = torch.from_numpy(np.asarray(inv_freq)).double().cuda() if inv_freq is not None else None
+        args = [self.dev16(a) if b is None else b
+                for a, b in ((self.q, q), (self.nk, k), (self.nv, v))]
+        return B.pkv_rope_append(self.desc, *args, f, self.gcu, self.max_new, self.gt, self.gctx,
+                                 self.max_ctx, interleaved=interleaved, mscale=mscale,
+                                 scales=self.gs, dev_err=self.err, **kw)
+
+    def positions(self):
+        return np.concatenate([np.arange(c - n, c) for n, c in zip(self.new, self.ctx)])
+
+    def oracle_append(self, inv_freq=(), interleaved=False, mscale=1.0):
+        """Appends on the host copies; returns (rotated q, rotated K)."""
+        pos = self.positions()
+        q = OS.rotate(self.q, pos, inv_freq, interleaved, mscale)
+        k = OS.rotate(self.nk, pos, inv_freq, interleaved, mscale)
+        f = max(np.float32(1), np.float32(1.41421356) * np.float32(abs(mscale))) if len(inv_freq) else 1.0
+        OS.append_scaled(self.k, self.scales, 0, k, self.nk, f, self.cu, self.tables, self.ctx)
+        OS.append_scaled(self.v, self.scales, 1, self.nv, self.nv, 1.0, self.cu, self.tables, self.ctx)
+        return q, k
+
+    def attention(self, scale):
+        return OS.attention(self.k, self.v, self.scales, self.q, self.cu, self.tables, self.ctx, scale)
+
+    def decode(self, scale, **kw):
+        return B.pkv_paged_attention_decode_scaled(self.desc, self.gs, self.dev16(self.q), self.gt,
+                                                   self.gctx, self.max_ctx, scale,
+                                                   dev_err=self.err, **kw)
+
+
+def freqs(rot, base=10000.0):
+    return base ** (-np.arange(0, rot, 2) / rot)
+
+
+def check_rotated(got, x, ref, m, dt, what):
+    """got (device) against ref, the rotation of x, within the bound above."""
+    got = got.double().cpu().numpy()
+    e = 2.0 ** -20 * abs(m) * 2 * np.abs(x).max(-1, keepdims=True)
+    half = torch.finfo(TD[dt]).eps / 2
+    tiny = 2.0 ** -25 if dt == W.F16 else 0.0
+    bad = np.abs(got - ref) > half * (np.abs(ref) + e) + e + tiny
+    assert not bad.any(), (what, int(bad.sum()), np.abs(got - ref).max())
+
+
+CASES = [
+    # dtype, heads, kv, D, bs, new, cached, rot, interleaved, mscale
+    (W.BF16, 4, 2, 128, 16, [1, 1, 1], [0, 16, 30], 128, False, 1.0),
+    (W.F16, 5, 5, 64, 16, [1, 1, 1, 1], [4, 15, 31, 63], 64, True, 1.0),
+    (W.BF16, 8, 1, 128, 32, [70, 1, 33, 0, 17], [0, 31, 7, 20, 96], 64, False, 1.3466),
+    (W.F16, 3, 3, 128, 8, [7, 8, 9, 1], [1, 0, 23, 7], 96, False, 0.5),
+    (W.F16, 6, 2, 64, 8, [40, 3], [5, 8], 16, True, 1.0),
+    (W.BF16, 2, 2, 64, 32, [5, 64, 100], [3, 0, 31], 48, False, 1.0),
+    (W.BF16, 17, 1, 128, 16, [19, 2], [1000, 2047], 0, False, 1.0),
+]
+
+
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_rope_append_scaled(i):
+    dt, h, kv, d, bs, new, cached, rot, inter, m = CASES[i]
+    b = Batch(40 + i, dt, h, kv, d, bs, new, cached, spread=1.5)
+    f = freqs(rot) if rot else ()
+    q = b.append(f if rot else None, inter, m)
+    torch.cuda.synchronize()
+    rq, rk = b.oracle_append(f, inter, m)
+    if not rot:
+        assert np.array_equal(H.to_bits(q), H.to_bits(b.dev16(b.q)))
+    check_rotated(q, b.q, rq, m if rot else 1.0, dt, "q")
+    gs = b.gs.cpu().numpy()
+    assert np.array_equal(gs, b.scales, equal_nan=True)
+    assert np.array_equal(b.gv.cpu().numpy(), b.v), "V codes"
+    gk = b.gk.cpu().numpy()
+    if not rot:
+        assert np.array_equal(gk, b.k), "K codes"
+    else:
+        # the new tokens' values; every other byte exactly
+        same = np.ones(gk.shape, bool)
+        row = 0
+        for s, c in enumerate(b.ctx):
+            for p in range(c - new[s], c):
+                phys, off = b.tables[s, p // bs], p % bs
+                same[phys, :, off] = False
+                sc = gs[phys, :, 0].astype(np.float64)[:, None]
+                got = oracle.decode(oracle.E4M3, gk[phys, :, off]) * sc
+                e = 2.0 ** -20 * abs(m) * 2 * np.abs(b.nk[row]).max(-1, keepdims=True)
+                bound = np.maximum(2.0 ** -4 * (np.abs(rk[row]) + e), 2.0 ** -10 * sc) + e
+                assert (np.abs(got - rk[row]) <= bound).all(), (s, p)
+                row += 1
+        assert np.array_equal(gk[same], b.k[same]), "bytes the call does not own"
+    assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("bs", [8, 16, 32])
+def test_rope_append_raises_the_scale_of_a_part_filled_block(bs):
+    """Each new token is twice the one before: every append after a block's
+    first raises the scale and re-rounds the codes before it, exactly as the
+    oracle does, and the neighbouring heads and blocks keep theirs."""
+    n = 2 * bs + 3
+    b = Batch(59, W.F16, 2, 2, 64, bs, [1], [n - 1], fill=False)
+    r = np.random.default_rng(59)
+    for p in range(n):
+        b.ctx = np.array([p + 1], np.int32)
+        b.gctx.fill_(p + 1)
+        x = r.standard_normal((1, 2, 64)) * 2.0 ** (p % 11 - 5)
+        x = torch.from_numpy(x).half().double().numpy()
+        before = b.scales.copy()
+        b.nk = b.nv = x
+        b.append(None)
+        b.oracle_append()
+        if p % bs and p % 11:
+            phys = b.tables[0, p // bs]
+            assert (b.scales[phys] >= before[phys]).all()
+    assert np.array_equal(b.gs.cpu().numpy(), b.scales, equal_nan=True)
+    assert np.array_equal(b.gk.cpu().numpy(), b.k) and np.array_equal(b.gv.cpu().numpy(), b.v)
+    assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("cache", [W.F16, W.BF16, W.E4M3])
+def test_rope_append_other_caches(cache):
+    """Caches without block scales: rotated K rounded once to the cache type,
+    V as pkv_kv_append writes it; strided inputs of one projection."""
+    dt = W.F16 if cache == W.E4M3 else cache
+    b = Batch(60, dt, 6, 2, 128, 16, [20, 1, 7], [3, 16, 0])
+    f = freqs(64)
+    shape = b.k.shape
+    if cache == W.E4M3:
+        kc, vc = b.gk, b.gv
+        desc = B.cache_desc(kc, vc, 0.03125, 0.0625)
+    else:
+        kc = torch.full(shape, float("nan"), dtype=TD[dt], device="cuda")
+        vc = kc.clone()
+        desc = B.cache_desc(kc, vc)
+    qkv = torch.cat([b.dev16(x) for x in (b.q, b.nk, b.nv)], 1)
+    q, k, v = qkv[:, :6], qkv[:, 6:8], qkv[:, 8:]
+    out = B.pkv_rope_append(desc, q, k, v, torch.from_numpy(f).cuda(), b.gcu, b.max_new, b.gt,
+                            b.gctx, b.max_ctx, dev_err=b.err)
+    pos = b.positions()
+    check_rotated(out, b.q, OS.rotate(b.q, pos, f), 1.0, dt, "q")
+    rk = OS.rotate(b.nk, pos, f)
+    seq = np.repeat(np.arange(3), b.new)
+    slots = b.tables[seq, pos // 16].astype(np.int64) * 16 + pos % 16
+    # V (and where it goes) exactly as the append without a rotation
+    k2, v2 = (torch.full_like(t, 0xff if cache == W.E4M3 else float("nan")) for t in (kc, vc))
+    d2 = B.cache_desc(k2, v2, desc.k_scale, desc.v_scale)
+    B.pkv_kv_append(d2, k.contiguous(), v.contiguous(), torch.from_numpy(slots).cuda())
+    if cache == W.E4M3:
+        same = (vc.cpu().numpy()[slots // 16, :, slots % 16] ==
+                v2.cpu().numpy()[slots // 16, :, slots % 16]).all()
+        got = oracle.decode(oracle.E4M3, kc.cpu().numpy()[slots // 16, :, slots % 16]) * 0.03125
+        e = 2.0 ** -20 * 2 * np.abs(b.nk).max(-1, keepdims=True)
+        sat = np.minimum(np.abs(rk), 448 * 0.03125) * np.sign(rk)
+        assert (np.abs(got - sat) <= np.maximum(2.0 ** -4 * (np.abs(rk) + e), 2.0 ** -10 * 0.03125) + e).all()
+        assert same
+    else:
+        assert np.array_equal(H.to_bits(vc), H.to_bits(v2))
+        i = torch.from_numpy(slots).cuda()
+        check_rotated(kc[i // 16, :, i % 16], b.nk, rk, 1.0, dt, "K")
+        # nothing else is written
+        assert np.array_equal(H.to_bits(kc.isnan()), H.to_bits(k2.isnan()))
+    assert int(b.err.item()) == 0
+
+
+def test_rope_append_far_positions_and_in_place():
+    """Positions past 2^24 (where an fp32 angle is off by radians), q rotated
+    in place, rows behind the last sequence untouched."""
+    d, bs = 64, 8
+    far = [(1 << 24) + 12345, (1 << 27) + 7]
+    r = np.random.default_rng(3)
+    q = r.standard_normal((4, 2, d)).astype(np.float16).astype(np.float64)
+    gq = torch.from_numpy(q).half().cuda()
+    # a table row long enough is all the call reads of the far blocks
+    nblk = far[1] // bs + 1
+    tables = torch.zeros(2, nblk, dtype=torch.int32, device="cuda")
+    tables[1, far[1] // bs] = 1
+    kc = torch.zeros(2, 2, bs, d, dtype=torch.float16, device="cuda")
+    vc = kc.clone()
+    ctx = torch.tensor([far[0] + 1, far[1] + 1], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    f = freqs(d)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = B.pkv_rope_append(B.cache_desc(kc, vc), gq, gq.clone(), gq.clone(),
+                            torch.from_numpy(f).cuda(), cu, 1, tables, ctx, far[1] + 1,
+                            dev_err=err, q_out=gq)
+    torch.cuda.synchronize()
+    ref = OS.rotate(q[:2], np.array(far), f)
+    check_rotated(out[:2], q[:2], ref, 1.0, W.F16, "far")
+    assert np.array_equal(out[2:].double().cpu().numpy(), q[2:])
+    assert int(err.item()) == 0
+
+
+def test_rope_append_without_q_and_non_finite_inputs():
+    b = Batch(61, W.BF16, 2, 2, 64, 16, [6, 1], [0, 3])
+    b.nv[1, 0, 5] = np.inf
+    b.nv[2, 1, 7] = -np.inf
+    b.nv[3, 0, 9] = np.nan
+    b.nv[4] = 0.0
+    b.nk[4] = 0.0
+    assert b.append(q=None, inv_freq=None) is not None
+    b2 = Batch(61, W.BF16, 2, 2, 64, 16, [6, 1], [0, 3])
+    out = B.pkv_rope_append(b2.desc, None, b.dev16(b.nk), b.dev16(b.nv), None, b2.gcu, b2.max_new,
+                            b2.gt, b2.gctx, b2.max_ctx, scales=b2.gs)
+    assert out is None
+    b.oracle_append()
+    for x in (b, b2):
+        assert np.array_equal(x.gs.cpu().numpy(), b.scales, equal_nan=True)
+        got = oracle.decode(oracle.E4M3, x.gv.cpu().numpy())
+        ref = oracle.decode(oracle.E4M3, b.v)
+        assert np.array_equal(got, ref, equal_nan=True)
+        assert np.array_equal(x.gk.cpu().numpy(), b.k)
+    phys = b.tables[0, 0]
+    assert oracle.decode(oracle.E4M3, b.v)[phys, 0, 1, 5] == 448
+
+
+def test_rope_append_bad_inputs_are_flagged_and_skipped():
+    b = Batch(62, W.F16, 2, 2, 64, 16, [5, 6, 7], [0, 30, 9])
+    before = (b.gk.clone(), b.gv.clone(), b.gs.clone())
+    ctx = b.ctx.copy()
+    ctx[0] = 3                                    # fewer tokens than new ones
+    b.gctx.copy_(torch.from_numpy(ctx))
+    t = b.tables.copy()
+    t[1, 2] = b.nb                                # outside the pool
+    b.gt.copy_(torch.from_numpy(t))
+    q_out = torch.full((18, 2, 64), 7.0, dtype=torch.float16, device="cuda")
+    b.append(freqs(64), q_out=q_out)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == B.PKV_DEVERR_CONTEXT | B.PKV_DEVERR_BLOCK_ID
+    assert (q_out[:5] == 7).all() and not (q_out[5:] == 7).all()
+    for a, c in zip(before, (b.gk, b.gv, b.gs)):
+        for s, blk in ((0, 0), (1, 2)):
+            i = int(b.tables[s, blk])
+            assert torch.equal(a[i].view(torch.uint8), c[i].view(torch.uint8))
+    rq = OS.rotate(b.q, b.positions(), freqs(64))
+    check_rotated(q_out[5:], b.q[5:], rq[5:], 1.0, W.F16, "other sequences")
+
+
+DECODE = [
+    # dtype, heads, kv, D, bs, ctx, partition, size of values, spread of rows (log2)
+    (W.F16, 8, 8, 64, 16, [5, 17, 33, 64], 0, 1.0, 0.0),
+    (W.BF16, 16, 2, 128, 16, [1, 300, 129, 0, 777], 0, 1.0, 1.0),
+    (W.BF16, 16, 2, 128, 16, [1, 300, 129, 0, 777], 64, 1.0, 1.0),
+    (W.F16, 3, 1, 128, 32, [1000, 31, 32, 33], 96, 0.01, 2.0),
+    (W.F16, 16, 1, 64, 8, [7, 8, 9, 200, 0], 16, 10.0, 1.0),
+    (W.BF16, 10, 1, 128, 8, [65, 511], 0, 1.0, 1.0),
+    (W.BF16, 5, 5, 64, 32, [2500, 1], 0, 1e-6, 1.0),
+    (W.F16, 4, 4, 128, 8, [15, 1023], 48, 1.0, 3.0),
+    (W.BF16, 14, 2, 64, 16, [0, 0, 1], 0, 1.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("i", range(len(DECODE)))
+def test_decode_scaled(i):
+    dt, h, kv, d, bs, ctx, part, size, spread = DECODE[i]
+    b = Batch(80 + i, dt, h, kv, d, bs, [1] * len(ctx), ctx, size=size, spread=spread)
+    # the contexts as cached (the row's own token is not appended here)
+    b.ctx = np.asarray(ctx, np.int32)
+    b.gctx.copy_(torch.from_numpy(b.ctx))
+    b.max_ctx = max(ctx)
+    out = b.decode(1 / np.sqrt(d), partition_size=part)
+    again = b.decode(1 / np.sqrt(d), partition_size=part)
+    torch.cuda.synchronize()
+    ref = b.attention(1 / np.sqrt(d))
+    # the bound is absolute and relative to values of size one
+    H.assert_attention_close(H.out_to_double(out) / size, ref / size, "decode scaled %d" % i, dt)
+    assert torch.equal(out, again)
+    assert int(b.err.item()) == 0
+
+
+def test_decode_scaled_large_ratio_of_scales():
+    """V of one block 2^12 larger than the others but with no weight (its keys
+    point away): the small blocks keep their precision."""
+    b = Batch(95, W.F16, 4, 1, 128, 16, [1], [160])
+    b.ctx = np.array([160], np.int32)
+    b.q[...] = np.abs(b.q)
+    big = b.tables[0, 4]
+    x = np.full((16, 1, 128), -8.0)
+    OS.append_scaled(b.k, b.scales, 0, x, x, 1.0, [0, 16], np.array([[big]]), [16])
+    x = b.values(16, 1, 4096.0, 0.0)
+    OS.append_scaled(b.v, b.scales, 1, x, x, 1.0, [0, 16], np.array([[big]]), [16])
+    b.upload()
+    out = b.decode(1.0)
+    ref = b.attention(1.0)
+    H.assert_attention_close(H.out_to_double(out), ref, "decode scaled ratio", W.F16)
+    assert np.abs(ref).max() < 8
+
+
+def test_decode_scaled_range_checks():
+    b = Batch(96, W.F16, 4, 2, 64, 16, [1, 1, 1], [40, 50, 60])
+    b.ctx = np.array([40, 50, 60], np.int32)
+    ref = b.attention(0.125)
+    t = b.tables.copy()
+    t[0, 1] = -7
+    b.gt.copy_(torch.from_numpy(t))
+    b.gctx.copy_(torch.tensor([40, 9999, 60], dtype=torch.int32))
+    out = b.decode(0.125, partition_size=32)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == B.PKV_DEVERR_BLOCK_ID | B.PKV_DEVERR_CONTEXT
+    assert (out[1] == 0).all() and not out.isnan().any()
+    H.assert_attention_close(H.out_to_double(out)[2:], ref[2:], "decode scaled good", W.F16)
+
+
+def test_copy_blocks_scaled():
+    """Copy-on-write in two layers and a swap through pinned host memory, byte
+    for byte, scales included; a bad pair is flagged and skipped."""
+    r = np.random.default_rng(4)
+    shape = (20, 3, 8, 64)
+    ks = [torch.from_numpy(r.integers(0, 256, shape).astype(np.uint8)).cuda() for _ in range(2)]
+    vs = [torch.from_numpy(r.integers(0, 256, shape).astype(np.uint8)).cuda() for _ in range(2)]
+    ss = [torch.from_numpy(r.standard_normal((20, 3, 2)).astype(np.float32)).cuda() for _ in range(2)]
+    ref = [[t.clone() for t in x] for x in (ks, vs, ss)]
+    pairs = [(1, 17), (1, 18), (5, 19), (20, 3), (4, -1)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    descs = [B.cache_desc(k, v) for k, v in zip(ks, vs)]
+    B.pkv_copy_blocks_scaled(descs, ss, torch.tensor(pairs, device="cuda"), dev_err=err)
+    for x in ref:
+        for t in x:
+            for a, c in pairs[:3]:
+                t[c] = t[a].clone()
+    for x, y in zip((ks, vs, ss), ref):
+        assert all(torch.equal(a, c) for a, c in zip(x, y))
+    assert int(err.item()) == B.PKV_DEVERR_COPY_PAIR
+    # out to the host and back to other blocks
+    hk = torch.zeros((6,) + shape[1:], dtype=torch.uint8).pin_memory()
+    hv, hs = hk.clone().pin_memory(), torch.zeros(6, 3, 2).pin_memory()
+    out = torch.tensor([(7, 2), (8, 0)], device="cuda")
+    B.pkv_copy_blocks_scaled(descs[0], ss[0], out, B.cache_desc(hk, hv), hs)
+    torch.cuda.synchronize()
+    assert torch.equal(hk[2], ks[0][7].cpu()) and torch.equal(hs[0], ss[0][8].cpu())
+    back = torch.tensor([(2, 9), (0, 10)], device="cuda")
+    B.pkv_copy_blocks_scaled(B.cache_desc(hk, hv), hs, back, descs[0], ss[0])
+    for x in (ks[0], vs[0], ss[0]):
+        assert torch.equal(x[9], x[7]) and torch.equal(x[10], x[8])
