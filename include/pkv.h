@@ -558,6 +558,22 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
                                              int32_t* dev_err, void* out, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Causal attention of prompts and chunks over a scaled cache:
+ * pkv_paged_attention_prefill with k_t and v_t = code * scale of their block and
+ * KV head.  q and out F16 or BF16, 1..128 query heads per KV head.  A block
+ * with a bad id reads as zeros; a token that a row may not see does not reach
+ * it, whatever its codes are.  A scale factor more than 2^22 below the largest
+ * of the context rounds its block's values to 2^-41 of the largest value.
+ * Device checks: as for the prefill.  Launches: one kernel.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_paged_attention_prefill_scaled(
+    const pkv_cache_desc* cache, const float* scales, const void* q, int32_t q_dtype,
+    int32_t num_seqs, int32_t num_heads, const int32_t* cu_seqlens_q, int32_t total_q,
+    int32_t max_q_len, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, int32_t max_context_len, float scale, int32_t* dev_err, void* out,
+    pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Copy of whole blocks with their scales, every layer: pkv_copy_blocks
  * (copy-on-write) inside one pool when dst is NULL, pkv_swap_blocks between two
  * pools otherwise (either may be pinned, device-mapped host memory; every

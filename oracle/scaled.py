@@ -88,5 +88,9 @@ def attention(k_codes, v_codes, scales, q, cu, tables, ctx, scale):
             hidden = np.arange(c)[None] > (c - n + np.arange(n))[:, None]
             x = np.where(hidden[:, None], -np.inf, x)
             p = np.exp(x - x.max(-1, keepdims=True))
-            out[rows, h * G:(h + 1) * G] = np.einsum("ngt,td->ngd", p / p.sum(-1, keepdims=True), v)
+            p = p / p.sum(-1, keepdims=True)
+            o = np.einsum("ngt,td->ngd", p, np.nan_to_num(v, nan=0.0))
+            # a NaN of V reaches exactly the rows that see its token
+            seen = (~hidden).astype(np.int64) @ np.isnan(v).astype(np.int64) > 0
+            out[rows, h * G:(h + 1) * G] = np.where(seen[:, None], np.nan, o)
     return out

@@ -12,5 +12,6 @@ from .binding import (  # noqa: F401
     pkv_paged_attention_decode_static_ws, pkv_paged_attention_partitions,
     pkv_paged_attention_prefill, pkv_shared_prefix_workspace_bytes, pkv_status_string,
     pkv_swap_blocks, pkv_copy_blocks_scaled, pkv_decode_scaled_partition_size,
-    pkv_decode_scaled_workspace_bytes, pkv_paged_attention_decode_scaled, pkv_rope_append,
+    pkv_decode_scaled_workspace_bytes, pkv_paged_attention_decode_scaled,
+    pkv_paged_attention_prefill_scaled, pkv_rope_append,
 )

@@ -88,6 +88,8 @@ def load():
         "pkv_decode_scaled_workspace_bytes": (ctypes.c_size_t, [dp, i32, i32, i32, i32]),
         "pkv_paged_attention_decode_scaled": (i32, [dp, vp, vp, i32, i32, i32, vp, i32, vp, i32,
                                                     f32, i32, vp, ctypes.c_size_t, vp, vp, vp]),
+        "pkv_paged_attention_prefill_scaled": (i32, [dp, vp, vp, i32, i32, i32, vp, i32, i32, vp,
+                                                     i32, vp, i32, f32, vp, vp, vp]),
         "pkv_copy_blocks_scaled": (i32, [dp, ctypes.POINTER(vp), dp, ctypes.POINTER(vp), i32, vp,
                                          i64, vp, vp]),
         "pkv_testing_set_decode_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),
@@ -509,6 +511,30 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
         _i32(context_lens, "context_lens").data_ptr(), max_context_len, scale, partition_size,
         _ptr(workspace), ws_bytes, _ptr(dev_err), out.data_ptr(), _stream(stream)),
         "pkv_paged_attention_decode_scaled")
+    return out
+
+
+def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len, block_tables,
+                                       context_lens, max_context_len, scale, dev_err=None,
+                                       out=None, stream=None):
+    """Causal attention over a scaled cache; arguments as
+    pkv_paged_attention_prefill."""
+    _dense(q, "q")
+    total, h, d = q.shape
+    num_seqs = context_lens.numel()
+    if d != cache.head_dim or cu_seqlens_q.numel() != num_seqs + 1 or \
+            block_tables.shape[0] != num_seqs:
+        raise ValueError("q, cu_seqlens_q, block_tables and context_lens do not fit together")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be dense and like q")
+    _check(load().pkv_paged_attention_prefill_scaled(
+        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), dtype_code(q.dtype),
+        num_seqs, h, _i32(cu_seqlens_q, "cu_seqlens_q").data_ptr(), total, max_q_len,
+        _i32(block_tables, "block_tables").data_ptr(), block_tables.shape[1],
+        _i32(context_lens, "context_lens").data_ptr(), max_context_len, scale, _ptr(dev_err),
+        out.data_ptr(), _stream(stream)), "pkv_paged_attention_prefill_scaled")
     return out
 
 

@@ -1,0 +1,714 @@
+// prefill_scaled.cu -- causal attention of prompts and chunks over an E4M3 cache
+// with a scale per block and KV head, on the 5th-generation tensor cores.
+//
+// Row j of sequence s, at position p = context_lens[s] - n_s + j, attends to
+// tokens t <= p of values code * scale.
+//
+// One CTA = two query tiles (a, b) of 128 (token, head) rows of one (sequence,
+// KV head), as in prefill_ws.cu, whose schedule this kernel keeps; new is how
+// operands come about.  Four warpgroups share the registers by setmaxnreg:
+//   * warps 12-15 (load and convert): walk the block table, read codes from
+//     global memory straight into registers one slot ahead, turn them into
+//     fp16 and store them into the 128-byte-swizzled operand tiles of a ring,
+//     slot j = K(j) and V(j - 1).  A byte read once is written as two: codes
+//     cross HBM and L2 at half a 16-bit cache's traffic.
+//     The scale goes into the conversion: a block's K becomes code * (ks / kref)
+//     2^7 with kref a power of two at or above the CTA's largest ks (V alike),
+//     which fp16 holds exactly while the scales are powers of two within 2^22
+//     of the largest; what falls below is under 2^-41 of the largest value.
+//     So one factor serves all scores, one all outputs, and the softmax does
+//     not know about blocks.
+//   * warps 8 and 10 (one issuing thread each): O_w += P_w(j-1) V(j-1), then
+//     S_w(j) = Q_w K(j)^T, taking turns by slot.
+//   * warps 0-3 and 4-7: softmax, one thread per row.  q is fp16 per row times
+//     a power of two (bf16 values fit without loss); the weights are fp16 (11
+//     bits, 2^-12 relative at most), so P V is one product for both types.
+// NaN codes of V: a weight of 0 times NaN would reach rows that may not see the
+// token, so the converter stores 0 and notes the first position of a NaN per
+// output column; rows at or past it get NaN there.
+// Every wait is bounded, as in prefill_ws.cu.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pkv_common.cuh"
+#include "scaled_internal.h"
+#include "tc_common.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;             // rows per query tile = tensor-memory lanes
+constexpr int kKeys = 128;             // keys per K/V tile
+constexpr int kMmaWarp = 8;            // issues query tile a's products; warp 10 b's
+constexpr int kConvWarp = 12;          // first of the four converting warps
+constexpr int kConvWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 176;
+constexpr int kMmaRegs = 40;
+constexpr int kConvRegs = 120;
+static_assert(2 * kSoftmaxRegs + kMmaRegs + kConvRegs <= 4 * kLaunchRegs, "register split");
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kUnit = 128.f;         // fp16 value of a code at the reference scale
+
+template <int D>
+struct Layout {
+    static constexpr int NP = D / 64;                  // 64-dim panels
+    static constexpr int ST = D == 128 ? 2 : 4;        // slots of the ring
+    static constexpr int QB = NP * kRows * 128;        // one query tile
+    static constexpr int KVB = NP * kKeys * 128;       // one K or V tile
+    static constexpr int q = 0;
+    static constexpr int slot = q + 2 * QB;            // [ST][K, V]
+    static constexpr int SLOT = 2 * KVB;
+    static constexpr int bytes = slot + ST * SLOT;
+    static constexpr int alloc = bytes + 1024;         // room to align the base
+    static constexpr uint32_t cols = 512;
+};
+
+template <int ST>
+struct Bars {
+    uint64_t q_full[2];      // 128 arrivals: the group's Q rows are in shared memory
+    uint64_t s_full[2];      // commit: S_w(kt) (and every earlier product of w) done
+    uint64_t p_full[2];      // 128 arrivals: P_w(kt) written
+    uint64_t o_full[2];      // commit: the last O_w += P_w V done
+    uint64_t full[ST];       // one arrival per converting warp: slot j is stored
+    uint64_t empty[ST];      // one arrival per issuing warp: slot j no longer read
+    uint64_t issued[2];      // issuing thread w has queued its products of slot j
+    uint64_t drain[2];       // commit: every product issued by warp w done
+};
+
+__device__ __forceinline__ bool aborted(const int* flag)
+{
+    return *reinterpret_cast<const volatile int*>(flag) != 0;
+}
+
+__device__ __forceinline__ void set_abort(int* flag, int32_t* dev_err)
+{
+    *reinterpret_cast<volatile int*>(flag) = 1;
+    flag_error(dev_err, PKV_DEVERR_TIMEOUT);
+}
+
+// Bounded wait by one thread; gives up early once another role has aborted.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, int* flag,
+                                         int32_t* dev_err)
+{
+    WaitClock clock;
+    for (uint32_t i = 0; i < kSpin; ++i) {
+        if (try_wait(bar, parity))
+            return true;
+        if (aborted(flag))
+            return false;
+        if (clock.expired(i))
+            break;
+    }
+    set_abort(flag, dev_err);
+    return false;
+}
+
+// The same by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* flag,
+                                          int32_t* dev_err)
+{
+    bool ok = false;
+    WaitClock clock;
+    for (uint32_t i = 0; i < kSpin; ++i) {
+        if (try_wait(bar, parity)) {
+            ok = true;
+            break;
+        }
+        if (aborted(flag) || clock.expired(i))
+            break;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok)
+        set_abort(flag, dev_err);
+    return ok;
+}
+
+// A power of two at or above every scale up to x (positive, finite; 1 for 0).
+__device__ __forceinline__ float reference_of(float x)
+{
+    const uint32_t e = __float_as_uint(x) & 0x7f800000u;
+    if (e == 0)
+        return 1.1754944e-38f;
+    return e >= 0x7e800000u ? 1.7014118e38f : __uint_as_float(e + 0x00800000u);
+}
+
+// code * f for 16 codes, as 16 fp16 values (f: the factor in both halves).
+__device__ __forceinline__ void convert16(const uint4& c, uint32_t f, uint4& lo, uint4& hi)
+{
+    auto mul = [f](uint32_t h) {
+        uint32_t r;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(f));
+        return r;
+    };
+    uint32_t a, b;
+    e4m3x4_to_f16x2(c.x, a, b);
+    lo.x = mul(a), lo.y = mul(b);
+    e4m3x4_to_f16x2(c.y, a, b);
+    lo.z = mul(a), lo.w = mul(b);
+    e4m3x4_to_f16x2(c.z, a, b);
+    hi.x = mul(a), hi.y = mul(b);
+    e4m3x4_to_f16x2(c.w, a, b);
+    hi.z = mul(a), hi.w = mul(b);
+}
+
+// Non-zero where a byte of w is a NaN code (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w)
+{
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t a, const uint4& v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+template <int QT_, int D, int BS>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_scaled_kernel(const __grid_constant__ ScaledPrefillParams sp)
+{
+    using L = Layout<D>;
+    constexpr int CT = QT_;                    // type of q and out
+    constexpr int ST = L::ST;
+    constexpr int NB = kKeys / BS;             // blocks per K/V tile
+    const PrefillParams& p = sp.p;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) Bars<ST> bars;
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_flag;
+    __shared__ uint32_t ref_bits[2];           // largest ks, vs of the CTA's blocks
+    __shared__ int nan_pos[D];                 // first key whose V is NaN in this column
+    __shared__ int any_nan;
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int G = p.group;
+    const int QT = kRows / G;                  // new tokens per query tile
+    const int span = 2 * QT;                   // new tokens per CTA
+    const int ntiles = (p.max_q_len + span - 1) / span;
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads;
+    const int64_t idx = blockIdx.x;
+    const int tile = ntiles - 1 - (int)(idx / units);      // heaviest tiles first
+    const int s = (int)((idx % units) / p.num_kv_heads);
+    const int g = (int)(idx % p.num_kv_heads);
+
+    const int cu0 = __ldg(p.cu_seqlens_q + s);
+    const int cu1 = __ldg(p.cu_seqlens_q + s + 1);
+    const int n = cu1 - cu0;
+    const int j0 = tile * span;
+    if (cu0 < 0 || cu1 < cu0 || cu1 > p.total_q) {
+        if (tid == 0 && tile == 0 && g == 0)
+            flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
+        return;
+    }
+    if (j0 >= n)
+        return;
+    const int ctx = __ldg(p.context_lens + s);
+    uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+    auto row_off = [&](int j, int h) -> int64_t {     // element offset of (token j, head h)
+        return ((int64_t)(cu0 + j) * p.num_heads + g * G + h) * D;
+    };
+    if (ctx < n || ctx > p.max_context_len || n > p.max_q_len ||
+        (ctx + BS - 1) / BS > p.max_blocks_per_seq) {
+        if (tid == 0 && j0 == 0 && g == 0)
+            flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
+        // zero rows; the last tile's CTA takes the rows no tile covers
+        const int last = tile == ntiles - 1 ? n : min(n, j0 + span);
+        for (int64_t i = tid; i < (int64_t)(last - j0) * G * (D / 2); i += blockDim.x) {
+            const int64_t r = i / (D / 2);
+            reinterpret_cast<uint32_t*>(out + row_off(j0 + (int)(r / G), (int)(r % G)))[i % (D / 2)] = 0u;
+        }
+        return;
+    }
+    // the two query tiles: tokens [j0 + w QT, j0 + w QT + ntok_w)
+    const int ntok0 = min(QT, n - j0);
+    const int ntok1 = max(0, min(QT, n - j0 - QT));
+    const int pos00 = ctx - n + j0;            // position of tile a's first token
+    const int pos01 = pos00 + QT;
+    const int nkv0 = (pos00 + ntok0 + kKeys - 1) / kKeys;
+    const int nkv1 = ntok1 > 0 ? (pos01 + ntok1 + kKeys - 1) / kKeys : 0;
+    const int nk = max(nkv0, nkv1);            // K/V tiles the CTA loads
+    const int kv_end = ntok1 > 0 ? pos01 + ntok1 : pos00 + ntok0;
+    const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+    const float2* scales = reinterpret_cast<const float2*>(sp.scales);
+
+    const uint32_t raw = s_addr(smem_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+
+    if (tid == 0) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            bar_init(s_addr(&bars.q_full[w]), kRows);
+            bar_init(s_addr(&bars.s_full[w]), 1);
+            bar_init(s_addr(&bars.p_full[w]), kRows);
+            bar_init(s_addr(&bars.o_full[w]), 1);
+        }
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            bar_init(s_addr(&bars.full[i]), kConvWarps);
+            bar_init(s_addr(&bars.empty[i]), ntok1 > 0 ? 2 : 1);
+        }
+        bar_init(s_addr(&bars.issued[0]), 1);
+        bar_init(s_addr(&bars.issued[1]), 1);
+        bar_init(s_addr(&bars.drain[0]), 1);
+        bar_init(s_addr(&bars.drain[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        abort_flag = 0;
+        any_nan = 0;
+        ref_bits[0] = ref_bits[1] = 0u;
+    }
+    if (tid < D)
+        nan_pos[tid] = 0x7fffffff;
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         s_addr(&tmem_holder)),
+                     "r"(L::cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    __syncthreads();
+    // the largest scales of the CTA's blocks
+    {
+        uint32_t mk = 0, mv = 0;
+        for (int b = tid; b * BS < kv_end; b += kThreads) {
+            const int phys = __ldg(table + b);
+            if (phys < 0 || (int64_t)phys >= p.num_blocks) {
+                flag_error(p.dev_err, PKV_DEVERR_BLOCK_ID);
+                continue;
+            }
+            const float2 sc = __ldg(scales + (int64_t)phys * p.num_kv_heads + g);
+            // positive floats order as their bits; anything else counts as 0
+            if (sc.x > 0.f)
+                mk = max(mk, __float_as_uint(sc.x));
+            if (sc.y > 0.f)
+                mv = max(mv, __float_as_uint(sc.y));
+        }
+        mk = __reduce_max_sync(0xffffffffu, mk);
+        mv = __reduce_max_sync(0xffffffffu, mv);
+        if (lane == 0) {
+            atomicMax(&ref_bits[0], mk);
+            atomicMax(&ref_bits[1], mv);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder;
+    const float kref = reference_of(__uint_as_float(ref_bits[0]));
+    const float vref = reference_of(__uint_as_float(ref_bits[1]));
+
+    if (warp < 8) {
+        // ---------------- softmax of query tile w ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int w = warp >> 2;
+        const int r = tid & (kRows - 1);
+        const int ntok = w ? ntok1 : ntok0;
+        if (ntok > 0) {
+            const int nrows = ntok * G;
+            const int jw = j0 + w * QT;
+            const int pos0 = w ? pos01 : pos00;
+            const int nkv = w ? nkv1 : nkv0;
+            float qk;                                  // this row's factor of the scores
+            {
+                // q in fp16, scaled to at most 2^14 in size; rows past the
+                // tile's are zero
+                const uint32_t qs = sb + L::q + w * L::QB;
+                const bool ok = r < nrows;
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +
+                                      (ok ? row_off(jw + r / G, r % G) : 0);
+                float up = 1.f;
+                uint4 v[D / 8];
+                float mx = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    v[c] = ok ? ld_ro(src + c * 8) : make_uint4(0, 0, 0, 0);
+                    float x[8];
+                    unpack_vec<CT>(v[c], x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        mx = fmaxf(mx, fabsf(x[e]));
+                }
+                if (mx > 0.f && mx < __builtin_huge_valf()) {
+                    const float ex = 13.f - (float)((int)(__float_as_uint(mx) >> 23) - 127);
+                    up = exp2f(fminf(fmaxf(ex, -120.f), 120.f));
+                }
+                // the factor of the scores stays positive: the scale's sign (or
+                // a scale of 0) goes into q
+                const float sign = p.qk_scale_log2 < 0.f ? -1.f : (p.qk_scale_log2 == 0.f ? 0.f : 1.f);
+                qk = sign == 0.f ? 1.f
+                                 : fabsf(p.qk_scale_log2) * (1.f / up) * (kref * (1.f / kUnit));
+                up *= sign;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    float x[8];
+                    unpack_vec<CT>(v[c], x);
+                    st_shared16(qs + panel_off(r, c, kRows),
+                                make_uint4(pack_rn<kF16>(x[0] * up, x[1] * up),
+                                           pack_rn<kF16>(x[2] * up, x[3] * up),
+                                           pack_rn<kF16>(x[4] * up, x[5] * up),
+                                           pack_rn<kF16>(x[6] * up, x[7] * up)));
+                }
+                async_proxy_fence();
+                bar_arrive(s_addr(&bars.q_full[w]));
+            }
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t t_s = tmem + lanes + 128u * w;
+            const uint32_t t_o = tmem + lanes + 256u + (uint32_t)D * w;
+            const int pos = pos0 + r / G;              // this row's position
+            float m_run = kNegInf;                     // running max of the scaled logits
+            float l_run = 0.f;
+            bool alive = true;
+            for (int kt = 0; kt < nkv; ++kt) {
+                if (!wait_warp(s_addr(&bars.s_full[w]), kt & 1, &abort_flag, p.dev_err)) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                float x[kKeys];
+#pragma unroll
+                for (int c0 = 0; c0 < kKeys; c0 += 16)
+                    tmem_ld16(t_s + c0, *reinterpret_cast<uint32_t(*)[16]>(x + c0));
+                tmem_wait_ld();
+                // causal mask only where some key passes some row's position
+                if (kt * kKeys + kKeys - 1 > pos0) {
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j)
+                        x[j] = kt * kKeys + j <= pos ? x[j] : kNegInf;
+                }
+                // row max: eight independent chains of three-input maxima
+                float mc[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    mc[i] = fmaxf(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+                for (int j = 16; j < kKeys; j += 16)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mc[i] = fmax3(mc[i], x[j + 2 * i], x[j + 2 * i + 1]);
+                const float mx = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]),
+                                       fmaxf(mc[6], mc[7]));
+                const float m_cand = fmaxf(m_run, mx * qk);
+                const bool raise = m_cand > m_run + 8.f;
+                const float m_new = raise ? m_cand : m_run;
+                const float alpha = raise ? fast_exp2(m_run - m_new) : 1.f;   // 0 on the first tile
+                if (kt > 0 && __any_sync(0xffffffffu, raise)) {
+                    // O_w += P_w(kt-1) V(kt-1) has completed: the commit behind
+                    // S_w(kt) covers every earlier product
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t r32[32];
+                        tmem_ld16(t_o + c0, *reinterpret_cast<uint32_t(*)[16]>(r32));
+                        tmem_ld16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(r32 + 16));
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            r32[j] = __float_as_uint(__uint_as_float(r32[j]) * alpha);
+                        tmem_st16(t_o + c0, *reinterpret_cast<uint32_t(*)[16]>(r32));
+                        tmem_st16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(r32 + 16));
+                    }
+                }
+                m_run = m_new;
+                const float2 qk2 = make_float2(qk, qk);
+                const float2 nm2 = make_float2(-m_new, -m_new);
+                float2 ls[4] = {};                     // four pairs of partial sums
+                // P over S: 16 keys as 8 columns of fp16 pairs at the start of
+                // those keys' own 16 columns
+#pragma unroll
+                for (int c0 = 0; c0 < kKeys; c0 += 16) {
+                    uint32_t hi[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // exp2(s qk - m); a masked key (-inf) gives 0
+                        const float2 t = ffma2(make_float2(x[c0 + 2 * e], x[c0 + 2 * e + 1]), qk2, nm2);
+                        const float2 pp = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                        ls[e & 3] = fadd2(ls[e & 3], pp);
+                        hi[e] = pack_rn<kF16>(pp.x, pp.y);
+                    }
+                    tmem_st8(t_s + c0, hi);
+                }
+                const float lsum = ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) +
+                                   ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+                tmem_wait_st();
+                l_run = l_run * alpha + lsum;
+                tc_fence_before();
+                bar_arrive(s_addr(&bars.p_full[w]));
+            }
+            if (alive)
+                alive = wait_warp(s_addr(&bars.o_full[w]), 0, &abort_flag, p.dev_err);
+            if (alive) {
+                // epilogue: O / l for this thread's row
+                tc_fence_after();
+                const float inv = l_run > 0.f ? (1.f / l_run) * (vref * (1.f / kUnit))
+                                              : (l_run == 0.f ? 0.f : l_run);
+                const bool nans = *reinterpret_cast<volatile int*>(&any_nan) != 0;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                    uint32_t r16[16];
+                    tmem_ld16(t_o + c0, r16);
+                    tmem_wait_ld();
+                    if (nans) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (*reinterpret_cast<volatile int*>(&nan_pos[c0 + e]) <= pos)
+                                r16[e] = 0x7fffffffu;
+                    }
+                    if (r < nrows) {
+                        uint32_t o8[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o8[e] = pack2(round_to<CT>(__uint_as_float(r16[2 * e]) * inv),
+                                          round_to<CT>(__uint_as_float(r16[2 * e + 1]) * inv));
+                        uint16_t* dst = out + row_off(jw + r / G, r % G) + c0;
+                        st_v4(dst, make_uint4(o8[0], o8[1], o8[2], o8[3]));
+                        st_v4(dst + 8, make_uint4(o8[4], o8[5], o8[6], o8[7]));
+                    }
+                }
+            }
+        }
+    } else if (warp < kConvWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if ((warp == kMmaWarp || warp == kMmaWarp + 2) && lane == 0 &&
+            (warp == kMmaWarp || ntok1 > 0)) {
+            // ---------------- tensor-core issue for query tile w (one thread) ----------------
+            // The two threads take turns by slot (a's P V of slot j, b's, a's of
+            // slot j + 1, ...; each thread's S follows its P V), so that one
+            // tile's softmax runs while the tensor core runs the other's products.
+            const int w = warp == kMmaWarp ? 0 : 1;
+            const int nkv = w ? nkv1 : nkv0;
+            const uint32_t id_s = instr_desc<kF16>(kRows, kKeys, 0);
+            const uint32_t id_o = instr_desc<kF16>(kRows, D, 1);
+            // descriptor halves: every K step only adds (bytes >> 4) to a low half
+            constexpr uint32_t hi1k = desc_hi(1024);
+            const uint32_t q_lo = desc_lo(sb + L::q + w * L::QB, 16);
+            const uint32_t k_lo = desc_lo(sb + L::slot, 16);
+            const uint32_t v_lo = desc_lo(sb + L::slot + L::KVB, kKeys * 128);
+            const uint32_t s_col = tmem + 128u * w;
+            const uint32_t o_col = tmem + 256u + (uint32_t)D * w;
+            bool alive = wait_one(s_addr(&bars.q_full[w]), 0, &abort_flag, p.dev_err);
+            for (int j = 0; alive && j <= nk; ++j) {
+                const uint32_t sl = (uint32_t)((j % ST) * L::SLOT >> 4);
+                if (!wait_one(s_addr(&bars.full[j % ST]), (j / ST) & 1, &abort_flag, p.dev_err))
+                    break;
+                const bool pv = j > 0 && j <= nkv;
+                if (pv && !wait_one(s_addr(&bars.p_full[w]), (j - 1) & 1, &abort_flag, p.dev_err))
+                    break;
+                if (w == 1 ? !wait_one(s_addr(&bars.issued[0]), j & 1, &abort_flag, p.dev_err)
+                           : (ntok1 > 0 && j > 0 &&
+                              !wait_one(s_addr(&bars.issued[1]), (j - 1) & 1, &abort_flag, p.dev_err)))
+                    break;
+                bool used = false;
+                if (pv) {
+                    tc_fence_after();
+                    const uint32_t acc0 = j > 1 ? 1u : 0u;
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        umma_ts_h(o_col, s_col + ks * 16, v_lo + sl + (uint32_t)(ks * 16 * 128 >> 4),
+                                  hi1k, id_o, ks > 0 ? 1u : acc0);
+                    if (j == nkv)
+                        umma_commit(s_addr(&bars.o_full[w]));
+                    used = true;
+                }
+                // the other thread may queue its P V while this one queues S
+                bar_arrive(s_addr(&bars.issued[w]));
+                if (j < nkv) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (uint32_t)(((ks >> 2) * kRows * 128 + (ks & 3) * 32) >> 4);
+                        const uint32_t offk = (uint32_t)(((ks >> 2) * kKeys * 128 + (ks & 3) * 32) >> 4);
+                        umma_h(s_col, q_lo + off, hi1k, k_lo + sl + offk, hi1k, id_s, ks > 0 ? 1u : 0u);
+                    }
+                    umma_commit(s_addr(&bars.s_full[w]));
+                    used = true;
+                }
+                // this thread no longer reads slot j once its products are done
+                if (used)
+                    umma_commit(s_addr(&bars.empty[j % ST]));
+                else
+                    bar_arrive(s_addr(&bars.empty[j % ST]));
+            }
+            // every product (and every commit's arrival) done before teardown
+            umma_commit(s_addr(&bars.drain[w]));
+            bar_wait(s_addr(&bars.drain[w]), 0);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+        // ---------------- load and convert (four warps) ----------------
+        constexpr int VPR = D / 16;                // 16-code vectors per row
+        constexpr int RPI = 32 / VPR;              // rows per warp access
+        constexpr int NV = kKeys / (RPI * kConvWarps);   // vectors a lane holds of a tile
+        const int cw = warp - kConvWarp;
+        const int c16 = lane % VPR;
+        const int rsub = cw * RPI + lane / VPR;    // row of the lane's vector 0
+        // D = 128: lanes of the second 64-dim panel store their halves in the
+        // other order, so that eight lanes never meet in a bank
+        const int flip = D == 128 ? c16 >> 2 : 0;
+        const int64_t tile_bytes = (int64_t)BS * D;
+        const unsigned char* kbase = reinterpret_cast<const unsigned char*>(p.k_cache) + g * tile_bytes;
+        const unsigned char* vbase = reinterpret_cast<const unsigned char*>(p.v_cache) + g * tile_bytes;
+        const int64_t stride = p.num_kv_heads * tile_bytes;
+        // lane i < NB: block i of a K/V tile: its id (-1: none) and its factors
+        struct Entry {
+            int phys;
+            uint32_t fk, fv;
+        };
+        auto entry = [&](int kt) -> Entry {
+            Entry e{-1, 0u, 0u};
+            const int tok = kt * kKeys + lane * BS;
+            if (lane < NB && tok < kv_end) {
+                const int phys = __ldg(table + tok / BS);
+                if (phys >= 0 && (int64_t)phys < p.num_blocks) {
+                    const float2 sc = __ldg(scales + (int64_t)phys * p.num_kv_heads + g);
+                    e.phys = phys;
+                    const float fk = sc.x / kref * kUnit, fv = sc.y / vref * kUnit;
+                    e.fk = pack_rn<kF16>(fk, fk);
+                    e.fv = pack_rn<kF16>(fv, fv);
+                }
+            }
+            return e;
+        };
+        uint4 kr[NV], vr[NV];
+        auto load = [&](const unsigned char* base, const Entry& e, int first, int end, uint4(&x)[NV]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int row = i * RPI * kConvWarps + rsub;
+                const int phys = __shfl_sync(0xffffffffu, e.phys, row / BS);
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (phys >= 0 && first + row < end)
+                    x[i] = ld_ro(base + phys * stride + (row % BS) * D + c16 * 16);
+            }
+        };
+        auto store = [&](uint32_t dst, uint32_t f, const uint4(&x)[NV]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int row = i * RPI * kConvWarps + rsub;
+                uint4 lo, hi;
+                convert16(x[i], __shfl_sync(0xffffffffu, f, row / BS), lo, hi);
+                st_shared16(dst + panel_off(row, 2 * c16 + flip, kKeys), flip ? hi : lo);
+                st_shared16(dst + panel_off(row, 2 * c16 + (flip ^ 1), kKeys), flip ? lo : hi);
+            }
+        };
+        Entry cur = entry(0), prev{-1, 0u, 0u};
+        load(kbase, cur, 0, kv_end, kr);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            vr[i] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j <= nk; ++j) {
+            const int st = j % ST;
+            const Entry next = j + 1 < nk ? entry(j + 1) : Entry{-1, 0u, 0u};
+            // NaN codes of V(j - 1): 0 in the tile, the position noted
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                bad |= nan_codes(vr[i].x) | nan_codes(vr[i].y) | nan_codes(vr[i].z) | nan_codes(vr[i].w);
+            if (bad != 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    uint32_t* w4 = reinterpret_cast<uint32_t*>(&vr[i]);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const uint32_t nc = nan_codes(w4[q4]);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (nc & (0x80u << (8 * b))) {
+                                atomicMin(&nan_pos[c16 * 16 + q4 * 4 + b],
+                                          (j - 1) * kKeys + i * RPI * kConvWarps + rsub);
+                                *reinterpret_cast<volatile int*>(&any_nan) = 1;
+                                w4[q4] &= ~(0xffu << (8 * b));
+                            }
+                    }
+                }
+            }
+            if (!wait_warp(s_addr(&bars.empty[st]), ((j / ST) & 1) ^ 1, &abort_flag, p.dev_err))
+                break;
+            const uint32_t dst = sb + L::slot + st * L::SLOT;
+            if (j < nk)
+                store(dst, cur.fk, kr);
+            if (j > 0)
+                store(dst + L::KVB, prev.fv, vr);
+            async_proxy_fence();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(s_addr(&bars.full[st]));
+            // the next slot's codes, before its wait
+            if (j + 1 < nk)
+                load(kbase, next, (j + 1) * kKeys, kv_end, kr);
+            if (j < nk)
+                load(vbase, cur, j * kKeys, kv_end, vr);
+            prev = cur;
+            cur = next;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(L::cols));
+    }
+}
+
+template <int QT, int D, int BS>
+cudaError_t run(const ScaledPrefillParams& sp, cudaStream_t stream)
+{
+    using L = Layout<D>;
+    const PrefillParams& p = sp.p;
+    auto kern = prefill_scaled_kernel<QT, D, BS>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
+        if (e != cudaSuccess)
+            return e;
+        configured[dev] = true;
+    }
+    const int span = 2 * (kRows / p.group);
+    const int64_t tiles = ((int64_t)p.max_q_len + span - 1) / span;
+    const int64_t ctas = tiles * p.num_seqs * p.num_kv_heads;
+    if (ctas > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    kern<<<(unsigned)ctas, kThreads, L::alloc, stream>>>(sp);
+    return cudaGetLastError();
+}
+
+template <int QT, int D>
+cudaError_t by_block(const ScaledPrefillParams& p, cudaStream_t st)
+{
+    switch (p.p.block_size) {
+    case 8: return run<QT, D, 8>(p, st);
+    case 16: return run<QT, D, 16>(p, st);
+    case 32: return run<QT, D, 32>(p, st);
+    default: return cudaErrorNotSupported;
+    }
+}
+
+template <int QT>
+cudaError_t by_dim(const ScaledPrefillParams& p, cudaStream_t st)
+{
+    return p.p.head_dim == 128 ? by_block<QT, 128>(p, st) : by_block<QT, 64>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_scaled(const ScaledPrefillParams& sp, cudaStream_t stream)
+{
+    if (sp.p.num_seqs <= 0 || sp.p.max_q_len <= 0)
+        return cudaSuccess;
+    if (sp.p.group < 1 || sp.p.group > kRows)
+        return cudaErrorNotSupported;
+    return sp.p.dtype == kF16 ? by_dim<kF16>(sp, stream) : by_dim<kBF16>(sp, stream);
+}
+
+}  // namespace pkv

@@ -98,6 +98,30 @@ def test_decode_scaled_checks(lib, desc, kw, want):
     assert lib.pkv_paged_attention_decode_scaled(ctypes.byref(_desc(**desc)), *a.values()) == want
 
 
+PREFILL = dict(scales=0x1000, q=0x2000, dtype=B.PKV_BF16, seqs=2, heads=64, cu=0x3000, total=10,
+               maxq=6, bt=0x4000, mb=64, ctx=0x5000, maxc=1000, scale=0.1, err=None, out=0x6000,
+               stream=None)
+
+
+@pytest.mark.parametrize("desc,kw,want", [
+    (dict(cache_dtype=B.PKV_BF16), {}, UNSUPPORTED),
+    (dict(block_size=12), {}, UNSUPPORTED),
+    (dict(num_kv_heads=6), {}, INVALID),
+    (dict(num_kv_heads=1), dict(heads=129), UNSUPPORTED),
+    (dict(), dict(scales=None), INVALID),
+    (dict(), dict(q=0x2004), INVALID),
+    (dict(), dict(cu=None), INVALID),
+    (dict(), dict(mb=0), INVALID),
+    (dict(), dict(maxc=(1 << 31) - 1), INVALID),
+    (dict(), dict(total=-1), INVALID),
+    (dict(), dict(total=0), B.PKV_OK),
+    (dict(), dict(maxq=0), B.PKV_OK),
+])
+def test_prefill_scaled_checks(lib, desc, kw, want):
+    a = dict(PREFILL, **kw)
+    assert lib.pkv_paged_attention_prefill_scaled(ctypes.byref(_desc(**desc)), *a.values()) == want
+
+
 def test_workspace_follows_the_partition(lib):
     d = _desc()
     assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 1000, 1008) == 0

@@ -117,6 +117,12 @@ class Batch:
                                                    dev_err=self.err, **kw)
 
 
+    def prefill(self, scale, **kw):
+        return B.pkv_paged_attention_prefill_scaled(self.desc, self.gs, self.dev16(self.q),
+                                                    self.gcu, self.max_new, self.gt, self.gctx,
+                                                    self.max_ctx, scale, dev_err=self.err, **kw)
+
+
 def freqs(rot, base=10000.0):
     return base ** (-np.arange(0, rot, 2) / rot)
 
@@ -384,6 +390,98 @@ def test_decode_scaled_range_checks():
     assert int(b.err.item()) == B.PKV_DEVERR_BLOCK_ID | B.PKV_DEVERR_CONTEXT
     assert (out[1] == 0).all() and not out.isnan().any()
     H.assert_attention_close(H.out_to_double(out)[2:], ref[2:], "decode scaled good", W.F16)
+
+
+PREFILL = [
+    # dtype, heads, kv, D, bs, new, cached, size, spread of rows (log2)
+    (W.BF16, 4, 4, 128, 16, [70, 1, 129, 64], [0, 0, 0, 0], 1.0, 1.0),
+    (W.F16, 4, 4, 128, 16, [300, 1, 257], [0, 0, 0], 1.0, 0.0),
+    (W.BF16, 8, 2, 64, 32, [33, 100, 7], [40, 0, 200], 10.0, 2.0),
+    (W.F16, 16, 2, 128, 8, [17, 65, 3, 0], [5, 130, 64, 9], 0.01, 1.0),
+    (W.BF16, 16, 1, 64, 16, [9, 20], [100, 0], 1e-6, 1.0),
+    (W.F16, 128, 1, 64, 16, [3, 2], [31, 0], 1.0, 1.0),
+    (W.BF16, 6, 2, 128, 16, [50, 23], [10, 77], 1.0, 3.0),
+    (W.F16, 2, 2, 64, 8, [600], [519], 1.0, 1.0),
+    (W.BF16, 7, 1, 128, 32, [1, 1, 130], [1000, 0, 31], 1.0, 1.0),
+]
+
+
+@pytest.mark.parametrize("i", range(len(PREFILL)))
+def test_prefill_scaled(i):
+    dt, h, kv, d, bs, new, cached, size, spread = PREFILL[i]
+    b = Batch(120 + i, dt, h, kv, d, bs, new, cached, size=size, spread=spread)
+    b.oracle_append()
+    b.upload()
+    out = b.prefill(1 / np.sqrt(d))
+    again = b.prefill(1 / np.sqrt(d))
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == 0
+    ref = b.attention(1 / np.sqrt(d))
+    H.assert_attention_close(H.out_to_double(out) / size, ref / size, "prefill scaled %d" % i, dt)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0])
+def test_attention_scaled_other_signs_of_the_scale(scale):
+    b = Batch(140, W.F16, 4, 2, 64, 16, [40, 1], [7, 30])
+    b.oracle_append()
+    b.upload()
+    H.assert_attention_close(H.out_to_double(b.prefill(scale)), b.attention(scale),
+                             "prefill scaled sign", W.F16)
+    b = Batch(141, W.F16, 4, 2, 64, 16, [1, 1], [70, 30])
+    b.oracle_append()
+    b.upload()
+    H.assert_attention_close(H.out_to_double(b.decode(scale)), b.attention(scale),
+                             "decode scaled sign", W.F16)
+
+
+def test_prefill_scaled_nan_of_a_later_token_stays_there():
+    """A NaN in K or V of a token reaches the rows that see the token (V: in its
+    own column) and no other."""
+    b = Batch(142, W.BF16, 4, 2, 64, 16, [150, 20], [3, 0])
+    b.nv[100, 1, 17] = np.nan
+    b.nk[120, 0, 5] = np.nan
+    b.oracle_append()
+    b.upload()
+    got = H.out_to_double(b.prefill(0.125))
+    ref = b.attention(0.125)
+    nan = np.isnan(ref)
+    assert nan.any() and not nan[:100].any() and not nan[150:].any()
+    assert np.array_equal(np.isnan(got), nan)
+    H.assert_attention_close(np.where(nan, 0, got), np.where(nan, 0, ref), "prefill nan", W.BF16)
+
+
+def test_prefill_scaled_range_checks():
+    b = Batch(143, W.F16, 4, 2, 64, 16, [40, 50, 300], [0, 10, 5])
+    b.oracle_append()
+    b.upload()
+    ref = b.attention(0.125)
+    t = b.tables.copy()
+    t[2, 10] = b.nb + 3                            # keys 160..175 of sequence 2
+    b.gt.copy_(torch.from_numpy(t))
+    c = b.ctx.copy()
+    c[0] = 39                                      # fewer tokens than new ones
+    b.gctx.copy_(torch.from_numpy(c))
+    out = b.prefill(0.125)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == B.PKV_DEVERR_BLOCK_ID | B.PKV_DEVERR_CONTEXT
+    assert (out[:40] == 0).all() and not out.isnan().any()
+    keep = np.r_[np.arange(40, 90), np.arange(90, 90 + 155)]
+    H.assert_attention_close(H.out_to_double(out)[keep], ref[keep], "prefill scaled good", W.F16)
+
+
+def test_prefill_scaled_padded_batch():
+    """Rows behind the last sequence, an empty sequence and a bound above every
+    length: rows that belong to nobody stay as they were."""
+    b = Batch(144, W.F16, 4, 2, 64, 16, [40, 0, 50], [0, 0, 10])
+    b.oracle_append()
+    b.upload()
+    q = torch.cat([b.dev16(b.q), torch.ones(7, 4, 64, dtype=torch.float16, device="cuda")])
+    out = torch.full_like(q, 3.0)
+    B.pkv_paged_attention_prefill_scaled(b.desc, b.gs, q, b.gcu, 1000, b.gt, b.gctx, b.max_ctx,
+                                         0.125, dev_err=b.err, out=out)
+    assert (out[90:] == 3).all() and int(b.err.item()) == 0
+    H.assert_attention_close(H.out_to_double(out[:90]), b.attention(0.125), "prefill padded", W.F16)
 
 
 def test_copy_blocks_scaled():
