@@ -128,8 +128,16 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
+# the current device and its current stream as plain numbers; the public call
+# makes a Stream object each time, several microseconds of a small call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return ctypes.c_void_p(_raw_stream(_raw_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -427,17 +435,21 @@ def _scales_of(cache, scales):
     return scales.data_ptr()
 
 
-def _token_rows(t, name, dtype=None, heads=None, dim=None, rows=None):
-    """Elements between the tokens of t [rows, heads, head_dim], whose heads lie
+def _on_device(t, name):
+    """A call runs on the current device; tensors of another are refused."""
+    i = t.get_device()
+    if i < 0 or i != (_raw_device() if _raw_device is not None else torch.cuda.current_device()):
+        raise ValueError("%s must be on the current CUDA device" % name)
+
+
+def _token_rows(t, name):
+    """(tokens, heads, head_dim, elements between tokens) of t, whose heads lie
     side by side (a slice of a fused projection will do)."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    n, h, d = t.shape
+    a, b, c = t.stride()
+    if c != 1 or (h > 1 and b != d):
         raise ValueError("%s must be [tokens, heads, head_dim] with dense heads" % name)
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("q, k and v must have the same type")
-    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim) or \
-            (rows is not None and t.shape[0] != rows):
-        raise ValueError("%s does not fit the cache or the other inputs" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return n, h, d, a if n > 1 else h * d
 
 
 def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tables, context_lens,
@@ -447,14 +459,18 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     q (None without q).  `inv_freq` is a float64 device tensor of rot_dim / 2
     radians per position (rope.inv_freq computes it), or None to rotate
     nothing; with `scales` the cache is a scaled one."""
-    rows = k.shape[0]
-    ks = _token_rows(k, "k", heads=cache.num_kv_heads, dim=cache.head_dim)
-    vs = _token_rows(v, "v", k.dtype, cache.num_kv_heads, cache.head_dim, rows)
-    qs, heads = 0, 0
+    rows, kv, d, ks = _token_rows(k, "k")
+    rows_v, kv_v, d_v, vs = _token_rows(v, "v")
+    if kv != cache.num_kv_heads or d != cache.head_dim or (rows_v, kv_v, d_v) != (rows, kv, d) or \
+            v.dtype != k.dtype:
+        raise ValueError("k and v must be alike and fit the cache")
+    qs = heads = 0
     if q is not None:
-        qs, heads = _token_rows(q, "q", k.dtype, dim=cache.head_dim, rows=rows), q.shape[1]
+        rows_q, heads, d_q, qs = _token_rows(q, "q")
+        if rows_q != rows or d_q != d or q.dtype != k.dtype:
+            raise ValueError("q must have the tokens, head_dim and type of k")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty((rows, heads, d), dtype=q.dtype, device=q.device)
         elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
             raise ValueError("q_out must be dense and like q")
     rot = 0
@@ -466,6 +482,9 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     num_seqs = context_lens.numel()
     if cu_seqlens_q.numel() != num_seqs + 1:
         raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
+    if block_tables.shape[0] != num_seqs:
+        raise ValueError("block_tables needs one row per sequence")
+    _on_device(k, "k")
     _check(load().pkv_rope_append(
         ctypes.byref(cache), _scales_of(cache, scales) if scales is not None else None,
         q.data_ptr() if q is not None else None, qs, k.data_ptr(), ks, v.data_ptr(), vs,
@@ -496,6 +515,7 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
     s, h, d = q.shape
     if d != cache.head_dim or context_lens.numel() != s or block_tables.shape[0] != s:
         raise ValueError("q, block_tables and context_lens do not fit together")
+    _on_device(q, "q")
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
@@ -525,6 +545,7 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
     if d != cache.head_dim or cu_seqlens_q.numel() != num_seqs + 1 or \
             block_tables.shape[0] != num_seqs:
         raise ValueError("q, cu_seqlens_q, block_tables and context_lens do not fit together")
+    _on_device(q, "q")
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
