@@ -7,10 +7,9 @@
 // One CTA = two query tiles (a, b) of 128 (token, head) rows of one (sequence,
 // KV head), as in prefill_ws.cu, whose schedule this kernel keeps; new is how
 // operands come about.  Four warpgroups share the registers by setmaxnreg:
-//   * warps 12-15 (load and convert): walk the block table, read codes from
-//     global memory straight into registers one slot ahead, turn them into
-//     fp16 and store them into the 128-byte-swizzled operand tiles of a ring,
-//     slot j = K(j) and V(j - 1).  A byte read once is written as two: codes
+//   * warps 12-15 (load and convert): walk the block table, copy codes one slot
+//     ahead, turn them into fp16 and store them into the 128-byte-swizzled
+//     operand tiles of a ring, slot j = K(j) and V(j - 1).  A byte read once is written as two: codes
 //     cross HBM and L2 at half a 16-bit cache's traffic.
 //     The scale goes into the conversion: a block's K becomes code * (ks / kref)
 //     2^7 with kref a power of two at or above the CTA's largest ks (V alike),
@@ -47,11 +46,12 @@ constexpr int kConvWarp = 12;          // first of the four converting warps
 constexpr int kConvWarps = 4;
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128;
-constexpr int kSoftmaxRegs = 176;
-constexpr int kMmaRegs = 40;
-constexpr int kConvRegs = 120;
+constexpr int kSoftmaxRegs = 184;
+constexpr int kMmaRegs = 48;
+constexpr int kConvRegs = 96;
 static_assert(2 * kSoftmaxRegs + kMmaRegs + kConvRegs <= 4 * kLaunchRegs, "register split");
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kBatch = 4;             // vectors a converting lane has in hand
 constexpr float kUnit = 128.f;         // fp16 value of a code at the reference scale
 
 template <int D>
@@ -63,7 +63,8 @@ struct Layout {
     static constexpr int q = 0;
     static constexpr int slot = q + 2 * QB;            // [ST][K, V]
     static constexpr int SLOT = 2 * KVB;
-    static constexpr int bytes = slot + ST * SLOT;
+    static constexpr int raw = slot + ST * SLOT;       // codes of one slot: K, V
+    static constexpr int bytes = raw + 2 * kKeys * D;
     static constexpr int alloc = bytes + 1024;         // room to align the base
     static constexpr uint32_t cols = 512;
 };
@@ -162,11 +163,33 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w)
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// w with its NaN codes cleared; each one's column gets the smallest position.
+__device__ __noinline__ uint32_t note_nans(uint32_t w, int* nan_pos, int* any_nan, int position)
+{
+    const uint32_t nc = nan_codes(w);
+    for (int b = 0; b < 4; ++b)
+        if (nc & (0x80u << (8 * b))) {
+            atomicMin(nan_pos + b, position);
+            *reinterpret_cast<volatile int*>(any_nan) = 1;
+            w &= ~(0xffu << (8 * b));
+        }
+    return w;
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t a, const uint4& v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
                  : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(a));
+    return r;
 }
 
 template <int QT_, int D, int BS>
@@ -401,16 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // O_w += P_w(kt-1) V(kt-1) has completed: the commit behind
                     // S_w(kt) covers every earlier product
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t r32[32];
-                        tmem_ld16(t_o + c0, *reinterpret_cast<uint32_t(*)[16]>(r32));
-                        tmem_ld16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(r32 + 16));
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t r16[16];              // (x stays live: few registers)
+                        tmem_ld16(t_o + c0, r16);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            r32[j] = __float_as_uint(__uint_as_float(r32[j]) * alpha);
-                        tmem_st16(t_o + c0, *reinterpret_cast<uint32_t(*)[16]>(r32));
-                        tmem_st16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(r32 + 16));
+                        for (int j = 0; j < 16; ++j)
+                            r16[j] = __float_as_uint(__uint_as_float(r16[j]) * alpha);
+                        tmem_st16(t_o + c0, r16);
                     }
                 }
                 m_run = m_new;
@@ -573,77 +594,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return e;
         };
-        uint4 kr[NV], vr[NV];
-        auto load = [&](const unsigned char* base, const Entry& e, int first, int end, uint4(&x)[NV]) {
+        // Codes travel through a staging area in which every thread has places of
+        // its own (vector i at i * 128 + thread): copied asynchronously one slot
+        // ahead, read back and converted by the thread that asked for them, so
+        // no barrier stands between.
+        const uint32_t raw_k = sb + L::raw + (tid - kConvWarp * 32) * 16;
+        const uint32_t raw_v = raw_k + kKeys * D;
+        constexpr int PITCH = 32 * kConvWarps * 16;
+        // start the copy of vector i of a tile whose first key is `first`
+        auto fetch = [&](uint32_t dst, const unsigned char* base, const Entry& e, int i, int first,
+                         int end) {
+            const int row = i * RPI * kConvWarps + rsub;
+            const int phys = __shfl_sync(0xffffffffu, e.phys, row / BS);
+            const bool ok = phys >= 0 && first + row < end;
+            cp16z(dst + i * PITCH,
+                  base + (ok ? (int64_t)phys * stride + (row % BS) * D + c16 * 16 : 0), ok);
+        };
+        // convert vectors i0 ... i0 + kBatch - 1, with their blocks' factors, into
+        // their places of an operand tile; a batch's reads, conversions and
+        // writes stand together, since one warp per scheduler has nothing but
+        // its own independent instructions to hide their latency
+        auto factors = [&](uint32_t f, int i0, uint32_t(&fi)[kBatch]) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int row = i * RPI * kConvWarps + rsub;
-                const int phys = __shfl_sync(0xffffffffu, e.phys, row / BS);
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (phys >= 0 && first + row < end)
-                    x[i] = ld_ro(base + phys * stride + (row % BS) * D + c16 * 16);
+            for (int u = 0; u < kBatch; ++u)
+                fi[u] = __shfl_sync(0xffffffffu, f, ((i0 + u) * RPI * kConvWarps + rsub) / BS);
+        };
+        auto store = [&](uint32_t dst, const uint32_t(&fi)[kBatch], int i0, const uint4(&x)[kBatch]) {
+            uint4 lo[kBatch], hi[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                convert16(x[u], fi[u], lo[u], hi[u]);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int row = (i0 + u) * RPI * kConvWarps + rsub;
+                st_shared16(dst + panel_off(row, 2 * c16 + flip, kKeys), flip ? hi[u] : lo[u]);
+                st_shared16(dst + panel_off(row, 2 * c16 + (flip ^ 1), kKeys), flip ? lo[u] : hi[u]);
             }
         };
-        auto store = [&](uint32_t dst, uint32_t f, const uint4(&x)[NV]) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int row = i * RPI * kConvWarps + rsub;
-                uint4 lo, hi;
-                convert16(x[i], __shfl_sync(0xffffffffu, f, row / BS), lo, hi);
-                st_shared16(dst + panel_off(row, 2 * c16 + flip, kKeys), flip ? hi : lo);
-                st_shared16(dst + panel_off(row, 2 * c16 + (flip ^ 1), kKeys), flip ? lo : hi);
-            }
-        };
-        Entry cur = entry(0), prev{-1, 0u, 0u};
-        load(kbase, cur, 0, kv_end, kr);
+        Entry prev{-1, 0u, 0u}, cur = entry(0), next = nk > 1 ? entry(1) : prev;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            vr[i] = make_uint4(0, 0, 0, 0);
+            fetch(raw_k, kbase, cur, i, 0, kv_end);
+        cp_async_commit();
         for (int j = 0; j <= nk; ++j) {
             const int st = j % ST;
-            const Entry next = j + 1 < nk ? entry(j + 1) : Entry{-1, 0u, 0u};
-            // NaN codes of V(j - 1): 0 in the tile, the position noted
-            uint32_t bad = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                bad |= nan_codes(vr[i].x) | nan_codes(vr[i].y) | nan_codes(vr[i].z) | nan_codes(vr[i].w);
-            if (bad != 0) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    uint32_t* w4 = reinterpret_cast<uint32_t*>(&vr[i]);
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const uint32_t nc = nan_codes(w4[q4]);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (nc & (0x80u << (8 * b))) {
-                                atomicMin(&nan_pos[c16 * 16 + q4 * 4 + b],
-                                          (j - 1) * kKeys + i * RPI * kConvWarps + rsub);
-                                *reinterpret_cast<volatile int*>(&any_nan) = 1;
-                                w4[q4] &= ~(0xffu << (8 * b));
-                            }
-                    }
-                }
-            }
+            const Entry after = j + 2 < nk ? entry(j + 2) : Entry{-1, 0u, 0u};
+            cp_async_wait<0>();
             if (!wait_warp(s_addr(&bars.empty[st]), ((j / ST) & 1) ^ 1, &abort_flag, p.dev_err))
                 break;
             const uint32_t dst = sb + L::slot + st * L::SLOT;
-            if (j < nk)
-                store(dst, cur.fk, kr);
-            if (j > 0)
-                store(dst + L::KVB, prev.fv, vr);
+            // each place is refilled for the next slot once its codes are used
+#pragma unroll
+            for (int i0 = 0; i0 < NV; i0 += kBatch) {
+                if (j < nk) {
+                    uint32_t fi[kBatch];
+                    uint4 x[kBatch];
+                    factors(cur.fk, i0, fi);
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        x[u] = lds16(raw_k + (i0 + u) * PITCH);
+                    store(dst, fi, i0, x);
+                    if (j + 1 < nk)
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u)
+                            fetch(raw_k, kbase, next, i0 + u, (j + 1) * kKeys, kv_end);
+                }
+            }
+#pragma unroll
+            for (int i0 = 0; i0 < NV; i0 += kBatch) {
+                if (j > 0) {
+                    uint32_t fi[kBatch];
+                    uint4 x[kBatch];
+                    factors(prev.fv, i0, fi);
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        x[u] = lds16(raw_v + (i0 + u) * PITCH);
+                        bad |= nan_codes(x[u].x) | nan_codes(x[u].y) | nan_codes(x[u].z) |
+                               nan_codes(x[u].w);
+                    }
+                    if (bad != 0) {
+                        // NaN codes: 0 in the tile, the position noted
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u) {
+                            uint32_t w4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                            for (int q4 = 0; q4 < 4; ++q4)
+                                w4[q4] = note_nans(w4[q4], nan_pos + c16 * 16 + q4 * 4, &any_nan,
+                                                   (j - 1) * kKeys + (i0 + u) * RPI * kConvWarps + rsub);
+                            x[u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                        }
+                    }
+                    __syncwarp();
+                    store(dst + L::KVB, fi, i0, x);
+                }
+                if (j < nk)
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        fetch(raw_v, vbase, cur, i0 + u, j * kKeys, kv_end);
+            }
+            cp_async_commit();
             async_proxy_fence();
             __syncwarp();
             if (lane == 0)
                 bar_arrive(s_addr(&bars.full[st]));
-            // the next slot's codes, before its wait
-            if (j + 1 < nk)
-                load(kbase, next, (j + 1) * kKeys, kv_end, kr);
-            if (j < nk)
-                load(vbase, cur, j * kKeys, kv_end, vr);
             prev = cur;
             cur = next;
+            next = after;
         }
+        cp_async_wait<0>();
     }
 
     tc_fence_before();
