@@ -533,10 +533,14 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
  * Decode attention over a scaled cache: pkv_paged_attention_decode with k_t and
  * v_t = code * scale of their block and KV head.  q and out F16 or BF16, 1..16
  * query heads per KV head; partition_size a multiple of block_size and of 16,
- * or 0.  The workspace has the layout given above, of
- * pkv_decode_scaled_workspace_bytes(...) bytes for the partition size of
- * pkv_decode_scaled_partition_size(...).  A block with a bad id contributes
- * nothing.  The same inputs and partition size give the same bits.
+ * or 0 for the library's choice: contexts up to 512 tokens one CTA each (one
+ * launch, no workspace), beyond that equal shares of the batch's tokens for the
+ * CTAs that fit the GPU at once, merged by a second launch.  An explicit
+ * partition_size gives the partitions, workspace layout and reduce of
+ * pkv_paged_attention_decode.  pkv_decode_scaled_partition_size tells the choice
+ * (0: equal shares), pkv_decode_scaled_workspace_bytes the scratch it needs.
+ * A block with a bad id contributes nothing.  The same inputs and partition
+ * size give the same bits on one kind of GPU.
  * Scales are positive and finite; V's small next to the largest of the context
  * lose no precision down to a ratio of 2^-20.
  * ------------------------------------------------------------------------- */

@@ -7,8 +7,8 @@
 // elements: ks multiplies the token's score, vs its softmax weight.  The codes
 // go to the tensor cores as fp16, in which every E4M3 value is exact.
 //
-// One CTA takes one partition of one sequence and KV head with up to 16 query
-// heads; its warps stride over the partition in steps of 16 tokens.  Lane
+// One CTA takes a run of tokens of one sequence and KV head with up to 16 query
+// heads; its warps stride over the run in steps of 16 tokens.  Lane
 // (g, t) = (lane / 4, lane % 4).
 //   * S^T = K Q^T (mma m16n8k16, fp16 in, fp32 out): rows = the 16 tokens,
 //     columns = 8 query heads.  The order of head_dim inside the dot product
@@ -41,7 +41,8 @@ using dec::kNegInf;
 using dec::PartitionWork;
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;              // query heads a CTA holds at most
+constexpr int kMaxGroup = 16;          // query heads per KV head
+constexpr int kOnePass = 512;          // tokens: contexts up to here are one CTA's work
 constexpr float kRaise = 8.f;          // log2: how far a score may pass the maximum
 constexpr float kWeightScale = 64.f;
 
@@ -97,7 +98,73 @@ __device__ __forceinline__ uint2 ld_stream8(const void* p)
     return r;
 }
 
-template <int QT, int D, int BS, int NNT>
+// Equal shares: tokens of every (sequence, KV head) in units of kUnit, laid end
+// to end (sequence, then head, then position); CTA c of C takes units
+// [c T / C, (c + 1) T / C) of the T there are, whatever items they belong to.
+// An item that one CTA holds whole is written out; a CTA has at most two
+// others, which it files as partials 2 c + 1 (starts at the item's first token)
+// and 2 c (starts inside the item), and the reduce kernel finds an item's
+// partials from the same arithmetic.
+constexpr int kUnit = 16 * kWarps;         // tokens: one step for each warp
+constexpr int kMinUnits = 4;               // smallest share
+constexpr int kMaxBalanced = 1024;         // sequences
+
+struct Shares {
+    int64_t total;                         // units
+    int64_t ctas;                          // CTAs that have any
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * total / ctas; }
+    __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * ctas - 1) / total; }
+};
+
+// Units of sequence s: 0 for an empty context and for one that cannot be used.
+__device__ __forceinline__ int units_of(const DecodeParams& p, int s, bool flag)
+{
+    const int ctx = __ldg(p.context_lens + s);
+    if (ctx < 0 || ctx > p.max_context_len || ctx > p.max_blocks_per_seq * p.block_size) {
+        if (flag)
+            flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
+        return 0;
+    }
+    return ceil_div_i(ctx, kUnit);
+}
+
+// first[s] = units before sequence s (of one KV head), first[num_seqs] = all;
+// called by every thread of a CTA of at least 32 threads.
+__device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, bool flag)
+{
+    if (threadIdx.x < 32) {
+        int carry = 0;
+        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+            const int s = s0 + threadIdx.x;
+            int v = s < p.num_seqs ? units_of(p, s, flag) : 0;
+            const int own = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if ((int)threadIdx.x >= o)
+                    v += u;
+            }
+            if (s < p.num_seqs)
+                first[s] = carry + v - own;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (threadIdx.x == 0)
+            first[p.num_seqs] = carry;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ Shares shares_of(const DecodeParams& p, const int* first, int64_t ctas)
+{
+    Shares sh;
+    sh.total = (int64_t)first[p.num_seqs] * p.num_kv_heads;
+    const int64_t most = (sh.total + kMinUnits - 1) / kMinUnits;
+    sh.ctas = most < ctas ? most : ctas;
+    return sh;
+}
+
+// BAL: equal shares; otherwise one CTA per (partition, sequence, KV head).
+template <int QT, int D, int BS, int NNT, bool BAL>
 __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     decode_scaled_kernel(const DecodeParams p, const float2* __restrict__ scales)
 {
@@ -106,51 +173,76 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     constexpr int NKV = D / 64;                // 16-byte vectors of a K row per lane
     constexpr int BPS = BS == 8 ? 2 : 1;       // blocks per step
     constexpr int SPB = BS == 32 ? 2 : 1;      // steps per block
+    constexpr int RT = 8 * NNT;                // rows
+    constexpr int PITCH = D + 2;               // (two-way conflicts at most)
 
-    extern __shared__ __align__(16) float smem[];
-    float* sm_m = smem;                        // [kWarps][16]
-    float* sm_l = sm_m + kWarps * kRows;
-    float* sm_acc = sm_l + kWarps * kRows;     // [kWarps][16][D]
-    __shared__ float sm_q[kRows];              // 1 / the heads' q scales
+    __shared__ float sm_m[kWarps][RT];
+    __shared__ float sm_l[kWarps][RT];
+    __shared__ float sm_q[RT];                 // 1 / the heads' q scales
+    __shared__ __align__(8) float sm_acc[kWarps * RT * PITCH];
     __shared__ uint2 sm_qf[NNT * NKS * 32];    // q fragments by lane
+    __shared__ int sm_first[BAL ? kMaxBalanced + 1 : 1];
 
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int g = lane >> 2;
     const int t = lane & 3;
     const int G = p.group;
-    int64_t idx = blockIdx.x;
-    const int head = (int)(idx % p.num_kv_heads);
-    idx /= p.num_kv_heads;
-    const int srank = (int)(idx % p.num_seqs);
-    const int part = (int)(idx / p.num_seqs);
 
-    // longest context first for batches of up to 128 sequences (ties by index)
-    int s = srank;
-    if (p.num_seqs <= 128) {
-        __shared__ int sh_ctx[128];
-        __shared__ int sh_seq;
-        for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x)
-            sh_ctx[i] = __ldg(p.context_lens + i);
-        __syncthreads();
-        for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) {
-            const int ci = sh_ctx[i];
-            int rank = 0;
-            for (int j = 0; j < p.num_seqs; ++j)
-                rank += (sh_ctx[j] > ci) || (sh_ctx[j] == ci && j < i);
-            if (rank == srank)
-                sh_seq = i;
-        }
-        __syncthreads();
-        s = sh_seq;
-    }
+    // what comes before in the stream may still write q, the cache and the tables
+    pdl_wait_primary();
     pdl_launch_dependents();
 
-    const PartitionWork w = dec::locate(p, s, part, threadIdx.x == 0);
-    if (w.idle || w.zero_out || w.zero_partial) {
-        if (!w.idle)
-            dec::write_trivial<QT>(p, w, head * G, G, threadIdx.x, blockDim.x);
-        return;
+    int64_t at = 0, end = 1;                   // BAL: the CTA's units
+    if constexpr (BAL) {
+        scan_units(p, sm_first, blockIdx.x == 0);
+        const Shares sh = shares_of(p, sm_first, gridDim.x);
+        if ((int64_t)blockIdx.x >= sh.ctas)
+            return;
+        at = sh.begin(blockIdx.x);
+        end = sh.begin(blockIdx.x + 1);
+    }
+    while (at < end) {
+    int s, head, t_begin, t_end;
+    bool direct;
+    int64_t prow;                              // first row of the partial
+    if constexpr (BAL) {
+        int lo = 0, hi = p.num_seqs;           // the last s with first[s] Hkv <= at
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((int64_t)sm_first[mid] * p.num_kv_heads <= at)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s = lo;
+        const int n = sm_first[s + 1] - sm_first[s];
+        const int64_t in = at - (int64_t)sm_first[s] * p.num_kv_heads;
+        head = (int)(in / n);
+        const int u0 = (int)(in - (int64_t)head * n);
+        const int u1 = (int)min((int64_t)n, u0 + (end - at));
+        t_begin = u0 * kUnit;
+        t_end = min(__ldg(p.context_lens + s), u1 * kUnit);
+        direct = u0 == 0 && u1 == n;
+        prow = (2 * (int64_t)blockIdx.x + (u0 == 0 ? 1 : 0)) * RT;
+        at += u1 - u0;
+    } else {
+        int64_t idx = blockIdx.x;
+        head = (int)(idx % p.num_kv_heads);
+        idx /= p.num_kv_heads;
+        s = (int)(idx % p.num_seqs);
+        const int part = (int)(idx / p.num_seqs);
+        const PartitionWork w = dec::locate(p, s, part, threadIdx.x == 0);
+        if (w.idle || w.zero_out || w.zero_partial) {
+            if (!w.idle)
+                dec::write_trivial<QT>(p, w, head * G, G, threadIdx.x, blockDim.x);
+            return;
+        }
+        t_begin = w.t_begin;
+        t_end = w.t_end;
+        direct = w.direct;
+        prow = dec::partial_row(p, s, head * G, w.slot);
+        at = end;
     }
 
     // q: each warp scales rows warp, warp + 4, ... by a power of two that
@@ -196,8 +288,6 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         for (int h = 0; h < 2; ++h)
             qk[n][h] = p.qk_scale_log2 * sm_q[8 * n + 2 * t + h];
 
-    const int t_begin = w.t_begin;
-    const int t_end = w.t_end;
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + t_begin / BS;
     const int nblk = ceil_div_i(t_end - t_begin, BS);
     const int nstep = ceil_div_i(t_end - t_begin, 16);
@@ -414,77 +504,213 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             const int r = 8 * n + 2 * t + h;
-            if (g == 0) {
-                sm_m[warp * kRows + r] = m_h[n][h];
-                sm_l[warp * kRows + r] = l;
-            }
-            float* o = sm_acc + (int64_t)(warp * kRows + r) * D + g * (D / 8);
+            if (r < G) {
+                if (g == 0) {
+                    sm_m[warp][r] = m_h[n][h];
+                    sm_l[warp][r] = l;
+                }
+                float* o = sm_acc + (warp * RT + r) * PITCH + g * (D / 8);
 #pragma unroll
-            for (int j = 0; j < NM; ++j) {
-                o[2 * j] = acc[n][j][h] * ov;
-                o[2 * j + 1] = acc[n][j][h + 2] * ov;
+                for (int j = 0; j < NM; ++j)
+                    *reinterpret_cast<float2*>(o + 2 * j) =
+                        make_float2(acc[n][j][h] * ov, acc[n][j][h + 2] * ov);
             }
         }
     __syncthreads();
-    dec::finish_rows<QT, kWarps, kRows>(p, w, head * G, G, sm_m, sm_l, sm_acc, threadIdx.x,
-                                        blockDim.x);
+    // merge of the warps, two dims a thread; warp i's weight is 2^(m_i - M)
+    for (int i = threadIdx.x; i < G * (D / 2); i += kWarps * 32) {
+        const int r = i / (D / 2);
+        const int d = (i - r * (D / 2)) * 2;
+        float M = sm_m[0][r];
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k)
+            M = fmaxf(M, sm_m[k][r]);
+        float L = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const float mk = sm_m[k][r];
+            const float f = mk == kNegInf ? 0.f : exp2_fast(mk - M);
+            const float2 o = *reinterpret_cast<const float2*>(sm_acc + (k * RT + r) * PITCH + d);
+            L += sm_l[k][r] * f;
+            o0 += o.x * f;
+            o1 += o.y * f;
+        }
+        if (direct) {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) +
+                                         ((int64_t)s * p.num_heads + head * G + r) * D + d) =
+                pack2(round_to<QT>(o0 * inv), round_to<QT>(o1 * inv));
+        } else {
+            // BAL: rows of one partial lie together; else heads are apart
+            const int64_t row = BAL ? prow + r : prow + (int64_t)r * p.max_partitions;
+            if (d == 0) {
+                p.ws_m[row] = M;
+                p.ws_l[row] = L;
+            }
+            *reinterpret_cast<float2*>(p.ws_o + row * D + d) = make_float2(o0, o1);
+        }
+    }
+    if (BAL)
+        __syncthreads();                       // the next item reuses the tables
+    }
+}
+
+// Merge of the partials of the equal shares: one warp per (sequence, query
+// head).  Items that one CTA held whole are left alone; sequences without
+// tokens (or with an unusable length) get zeros.
+constexpr int kReduceRows = 4;
+
+template <int QT, int D>
+__global__ void __launch_bounds__(kReduceRows * 32)
+    reduce_shares_kernel(const DecodeParams p, int64_t grid, int rows_per_partial)
+{
+    constexpr int DPL = D / 32;
+    __shared__ int sm_first[kMaxBalanced + 1];
+    scan_units(p, sm_first, false);
+    const Shares sh = shares_of(p, sm_first, grid);
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kReduceRows + (threadIdx.x >> 5);
+    if (row >= (int64_t)p.num_seqs * p.num_heads)
+        return;
+    const int s = (int)(row / p.num_heads);
+    const int hq = (int)(row - (int64_t)s * p.num_heads);
+    const int head = hq / p.group;
+    const int r = hq - head * p.group;
+    const int n = sm_first[s + 1] - sm_first[s];
+    float acc[DPL];
+#pragma unroll
+    for (int e = 0; e < DPL; ++e)
+        acc[e] = 0.f;
+    float L = 0.f;
+    pdl_wait_primary();
+    if (n > 0) {
+        const int64_t x = (int64_t)sm_first[s] * p.num_kv_heads + (int64_t)head * n;
+        const int64_t c0 = sh.owner(x);
+        const int64_t c1 = sh.owner(x + n - 1);
+        if (c0 == c1)
+            return;
+        float M = kNegInf;
+        for (int64_t c = c0 + lane; c <= c1; c += 32)
+            M = fmaxf(M, p.ws_m[(2 * c + (c == c0 ? 1 : 0)) * rows_per_partial + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+        for (int64_t c = c0; c <= c1; ++c) {
+            const int64_t pr = (2 * c + (c == c0 ? 1 : 0)) * rows_per_partial + r;
+            const float m = p.ws_m[pr];
+            const float f = m == kNegInf ? 0.f : exp2_fast(m - M);
+            L += f * p.ws_l[pr];
+            const float* o = p.ws_o + pr * D + lane * DPL;
+            if constexpr (DPL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(o);
+                acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(o);
+                acc[0] += f * v.x, acc[1] += f * v.y;
+            }
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row * D + lane * DPL;
+#pragma unroll
+    for (int e = 0; e < DPL; e += 2)
+        *reinterpret_cast<uint32_t*>(out + e) =
+            pack2(round_to<QT>(acc[e] * inv), round_to<QT>(acc[e + 1] * inv));
+}
+
+// The kernels here start while what precedes them in the stream ends, and wait
+// for it before they read anything it may write.
+template <class... Args>
+cudaError_t launch_early(void (*kern)(Args...), int64_t ctas, int threads, cudaStream_t stream,
+                         Args... args)
+{
+    if (ctas > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int QT, int D, int BS, int NNT>
-cudaError_t run(const DecodeParams& p, const float* scales, cudaStream_t stream)
+cudaError_t run(const DecodeParams& p, const float* scales, int sms, cudaStream_t stream)
 {
-    auto kern = decode_scaled_kernel<QT, D, BS, NNT>;
-    const int smem = (2 * kWarps * kRows + kWarps * kRows * D) * (int)sizeof(float);
-    const int64_t ctas = (int64_t)p.grid_partitions * p.num_seqs * p.num_kv_heads;
-    if (ctas > 0x7fffffffLL)
-        return cudaErrorInvalidConfiguration;
-    kern<<<(unsigned)ctas, kWarps * 32, smem, stream>>>(p, reinterpret_cast<const float2*>(scales));
-    return cudaGetLastError();
+    const float2* sc = reinterpret_cast<const float2*>(scales);
+    if (p.partition_size > 0)
+        return launch_early(decode_scaled_kernel<QT, D, BS, NNT, false>,
+                            (int64_t)p.grid_partitions * p.num_seqs * p.num_kv_heads, kWarps * 32,
+                            stream, p, sc);
+    const int64_t ctas = decode_scaled_ctas(p.group, sms);
+    cudaError_t e = launch_early(decode_scaled_kernel<QT, D, BS, NNT, true>, ctas, kWarps * 32,
+                                 stream, p, sc);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
+    return launch_early(reduce_shares_kernel<QT, D>, (rows + kReduceRows - 1) / kReduceRows,
+                        kReduceRows * 32, stream, p, ctas, 8 * NNT);
 }
 
 template <int QT, int D, int BS>
-cudaError_t by_group(const DecodeParams& p, const float* scales, cudaStream_t st)
+cudaError_t by_group(const DecodeParams& p, const float* scales, int sms, cudaStream_t st)
 {
-    return p.group <= 8 ? run<QT, D, BS, 1>(p, scales, st) : run<QT, D, BS, 2>(p, scales, st);
+    return p.group <= 8 ? run<QT, D, BS, 1>(p, scales, sms, st)
+                        : run<QT, D, BS, 2>(p, scales, sms, st);
 }
 
 template <int QT, int D>
-cudaError_t by_block(const DecodeParams& p, const float* scales, cudaStream_t st)
+cudaError_t by_block(const DecodeParams& p, const float* scales, int sms, cudaStream_t st)
 {
     switch (p.block_size) {
-    case 8: return by_group<QT, D, 8>(p, scales, st);
-    case 16: return by_group<QT, D, 16>(p, scales, st);
-    case 32: return by_group<QT, D, 32>(p, scales, st);
+    case 8: return by_group<QT, D, 8>(p, scales, sms, st);
+    case 16: return by_group<QT, D, 16>(p, scales, sms, st);
+    case 32: return by_group<QT, D, 32>(p, scales, sms, st);
     default: return cudaErrorNotSupported;
     }
 }
 
 template <int QT>
-cudaError_t by_dim(const DecodeParams& p, const float* scales, cudaStream_t st)
+cudaError_t by_dim(const DecodeParams& p, const float* scales, int sms, cudaStream_t st)
 {
-    return p.head_dim == 128 ? by_block<QT, 128>(p, scales, st) : by_block<QT, 64>(p, scales, st);
+    return p.head_dim == 128 ? by_block<QT, 128>(p, scales, sms, st)
+                             : by_block<QT, 64>(p, scales, sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_scaled(const DecodeParams& p, const float* scales, cudaStream_t stream)
+cudaError_t launch_decode_scaled(const DecodeParams& p, const float* scales, int sms,
+                                 cudaStream_t stream)
 {
     if (p.num_seqs <= 0)
         return cudaSuccess;
-    if (p.group < 1 || p.group > kRows)
+    if (p.group < 1 || p.group > kMaxGroup)
         return cudaErrorNotSupported;
-    return p.q_dtype == kF16 ? by_dim<kF16>(p, scales, stream) : by_dim<kBF16>(p, scales, stream);
+    return p.q_dtype == kF16 ? by_dim<kF16>(p, scales, sms, stream)
+                             : by_dim<kBF16>(p, scales, sms, stream);
 }
 
-// Tokens per partition: one partition per context when the (sequence, KV head)
-// items alone fill the GPU twice, else about 128 KiB of K and V codes per item.
-int32_t decode_scaled_partition(const DecodeParams& p, int sms)
+// Resident CTAs: the registers of three fit an SM with 8 heads, of two with 16.
+int64_t decode_scaled_ctas(int32_t group, int sms) { return (group <= 8 ? 3 : 2) * (int64_t)sms; }
+
+int64_t decode_scaled_partial_rows(int32_t group, int sms)
 {
-    const int32_t bs = p.block_size;
-    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads;
-    if (items >= 6LL * sms && p.max_context_len <= 8192)
+    return 2 * decode_scaled_ctas(group, sms) * (group <= 8 ? 8 : 16);
+}
+
+// One CTA per (sequence, KV head), in one launch, while the longest context is
+// short; equal shares beyond, unless there are more sequences than a CTA scans.
+int32_t decode_scaled_partition(const DecodeParams& p)
+{
+    const int32_t bs = p.block_size < 16 ? 16 : p.block_size;
+    if (p.max_context_len <= kOnePass)
         return (p.max_context_len + bs - 1) / bs * bs;
-    return (1 << 17) / (2 * p.head_dim);
+    return p.num_seqs <= kMaxBalanced ? 0 : (1 << 19) / (2 * p.head_dim);
 }
 
 }  // namespace pkv

@@ -76,15 +76,22 @@ struct Layout {
     int64_t parts, l_off, o_off, bytes;
 };
 
-// The decode workspace of pkv.h: m, l, o partials of every (sequence, head).
-Layout layout(int32_t num_seqs, int32_t num_heads, int32_t head_dim, int32_t max_context_len,
-              int32_t partition)
+// The decode workspace: m, l, o partials of every (sequence, head) and
+// partition as in pkv.h, or (partition 0) those of the equal shares.
+Layout layout(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t head_dim,
+              int32_t max_context_len, int32_t partition)
 {
     Layout w{};
-    w.parts = ((int64_t)max_context_len + partition - 1) / partition;
-    if (w.parts <= 1)
-        return w;
-    const int64_t rows = (int64_t)num_seqs * num_heads * w.parts;
+    int64_t rows;
+    if (partition == 0) {
+        w.parts = 1;
+        rows = pkv::decode_scaled_partial_rows(group, device_sms());
+    } else {
+        w.parts = ((int64_t)max_context_len + partition - 1) / partition;
+        if (w.parts <= 1)
+            return w;
+        rows = (int64_t)num_seqs * num_heads * w.parts;
+    }
     w.l_off = round_up(4 * rows, 256);
     w.o_off = 2 * w.l_off;
     w.bytes = w.o_off + round_up(4 * rows * head_dim, 256);
@@ -103,14 +110,14 @@ int32_t partition_of(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_head
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
     p.max_context_len = max_context_len;
-    return pkv::decode_scaled_partition(p, device_sms());
+    return pkv::decode_scaled_partition(p);
 }
 
 bool sizes_known(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads,
                  int32_t max_context_len, int32_t partition_size)
 {
     return c != nullptr && c->num_kv_heads > 0 && c->block_size > 0 && c->head_dim > 0 &&
-           num_seqs > 0 && num_heads > 0 && max_context_len > 0 && partition_size >= 0 &&
+           num_seqs > 0 && num_heads >= c->num_kv_heads && max_context_len > 0 && partition_size >= 0 &&
            max_context_len <= INT_MAX - 1024;
 }
 
@@ -223,7 +230,9 @@ size_t pkv_decode_scaled_workspace_bytes(const pkv_cache_desc* cache, int32_t nu
         return 0;
     const int32_t part =
         partition_of(cache, num_seqs, num_heads, max_context_len, partition_size);
-    return (size_t)layout(num_seqs, num_heads, cache->head_dim, max_context_len, part).bytes;
+    return (size_t)layout(num_seqs, num_heads, num_heads / cache->num_kv_heads, cache->head_dim,
+                          max_context_len, part)
+        .bytes;
 }
 
 pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const float* scales,
@@ -254,7 +263,8 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
         max_context_len > 0
             ? partition_of(cache, num_seqs, num_heads, max_context_len, partition_size)
             : 32;
-    const Layout wl = layout(num_seqs, num_heads, cache->head_dim, max_context_len, part);
+    const Layout wl = layout(num_seqs, num_heads, num_heads / cache->num_kv_heads, cache->head_dim,
+                             max_context_len, part);
     if (wl.bytes > 0 && (workspace == nullptr || !aligned(workspace, 256) ||
                          (int64_t)workspace_bytes < wl.bytes))
         return PKV_ERR_WORKSPACE;
@@ -290,8 +300,8 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
     p.dev_err = dev_err;
     p.out = out;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    st = from_cuda(pkv::launch_decode_scaled(p, scales, cs));
-    if (st != PKV_OK || wl.bytes == 0)
+    st = from_cuda(pkv::launch_decode_scaled(p, scales, device_sms(), cs));
+    if (st != PKV_OK || wl.bytes == 0 || part == 0)
         return st;
     pkv::ReduceParams r{};
     r.num_seqs = num_seqs;

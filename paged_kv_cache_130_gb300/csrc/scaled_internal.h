@@ -45,9 +45,15 @@ struct RopeParams {
 
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream);
 
-// Decode over a scaled cache: `p` with k_scale = v_scale = 1.
-cudaError_t launch_decode_scaled(const DecodeParams& p, const float* scales, cudaStream_t stream);
-int32_t decode_scaled_partition(const DecodeParams& p, int sms);
+// Decode over a scaled cache: `p` with k_scale = v_scale = 1; partition_size 0:
+// equal shares, whose partials take decode_scaled_partial_rows rows of ws_m,
+// ws_l and ws_o, and which launches its own reduce.
+cudaError_t launch_decode_scaled(const DecodeParams& p, const float* scales, int sms,
+                                 cudaStream_t stream);
+int64_t decode_scaled_ctas(int32_t group, int sms);
+int64_t decode_scaled_partial_rows(int32_t group, int sms);
+// The library's choice: tokens per partition, or 0 for equal shares.
+int32_t decode_scaled_partition(const DecodeParams& p);
 
 struct ScaledPrefillParams {
     PrefillParams p;               // dtype = that of q and out

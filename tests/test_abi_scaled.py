@@ -127,8 +127,15 @@ def test_workspace_follows_the_partition(lib):
     assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 1000, 1008) == 0
     ml = -(-4 * 4 * 64 * 16 // 256) * 256
     assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 1000, 64) == 2 * ml + 4 * 4 * 64 * 16 * 128
-    p = B.pkv_decode_scaled_partition_size(d, 4, 64, 1000)
-    assert p > 0 and p % 16 == 0
+    # the library's choice: one partition, without a workspace, for short
+    # contexts; equal shares beyond, of a size that the batch does not change
+    assert B.pkv_decode_scaled_partition_size(d, 4, 64, 500) == 512
+    assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 500) == 0
+    assert B.pkv_decode_scaled_partition_size(d, 4, 64, 1000) == 0
+    n = B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 1000)
+    assert n > 0 and n == B.pkv_decode_scaled_workspace_bytes(d, 900, 64, 100000)
+    p = B.pkv_decode_scaled_partition_size(d, 2000, 64, 1000)
+    assert p > 0 and p % 32 == 0
     assert B.pkv_decode_scaled_workspace_bytes(d, 0, 64, 1000) == 0
 
 

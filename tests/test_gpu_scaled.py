@@ -359,6 +359,88 @@ def test_decode_scaled(i):
     assert int(b.err.item()) == 0
 
 
+@pytest.mark.parametrize("heads,kv,d,bs,n,hi", [(6, 2, 64, 8, 40, 1500), (16, 1, 128, 16, 3, 4000),
+                                                (4, 4, 128, 32, 9, 2000), (8, 1, 64, 16, 1, 5000)])
+def test_decode_scaled_equal_shares(heads, kv, d, bs, n, hi):
+    """Ragged batches whose items are cut at every kind of place: empty
+    contexts, unusable ones (zeros, flagged), whole items, long ones; a
+    workspace full of NaN."""
+    r = np.random.default_rng(100 + n)
+    ctx = r.integers(0, hi, n).astype(np.int32)
+    ctx[-1] = hi
+    if n > 5:
+        ctx[2] = 0
+    b = Batch(97, W.BF16, heads, kv, d, bs, [1] * n, ctx, spread=1.0)
+    b.ctx = ctx
+    b.max_ctx = hi
+    seen = ctx.copy()
+    if n > 5:
+        seen[4], seen[5] = -1, hi + 1              # flagged
+        ctx[4] = ctx[5] = 0
+    b.gctx.copy_(torch.from_numpy(seen))
+    assert B.pkv_decode_scaled_partition_size(b.desc, n, heads, hi) == 0
+    ws = torch.full((B.pkv_decode_scaled_workspace_bytes(b.desc, n, heads, hi),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    out = b.decode(0.11, workspace=ws)
+    again = b.decode(0.11)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == (B.PKV_DEVERR_CONTEXT if n > 5 else 0)
+    H.assert_attention_close(H.out_to_double(out), b.attention(0.11), "equal shares %d" % n, W.BF16)
+    assert torch.equal(out, again)
+
+
+def test_scaled_calls_in_graphs_and_on_another_stream():
+    """An append, decode and prefill captured once and replayed after the inputs
+    changed in place, while other calls use the same workspace on the capture's
+    stream in between."""
+    b = Batch(98, W.BF16, 8, 2, 64, 16, [1, 1, 1], [700, 30, 1200])
+    f = torch.from_numpy(freqs(64)).cuda()
+    ws = torch.empty(B.pkv_decode_scaled_workspace_bytes(b.desc, 3, 8, b.max_ctx), dtype=torch.uint8,
+                     device="cuda")
+    q, k, v = (b.dev16(x) for x in (b.q, b.nk, b.nv))
+    qr, out, pre = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+
+    def step():
+        B.pkv_rope_append(b.desc, q, k, v, f, b.gcu, 1, b.gt, b.gctx, b.max_ctx, scales=b.gs,
+                          q_out=qr, dev_err=b.err)
+        B.pkv_paged_attention_decode_scaled(b.desc, b.gs, qr, b.gt, b.gctx, b.max_ctx, 0.125,
+                                            workspace=ws, out=out, dev_err=b.err)
+        B.pkv_paged_attention_prefill_scaled(b.desc, b.gs, qr, b.gcu, 1, b.gt, b.gctx, b.max_ctx,
+                                             0.125, out=pre, dev_err=b.err)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            step()
+    torch.cuda.synchronize()
+    for i in range(3):
+        x = b.values(3, 8, 1.0, 0.0)
+        b.q = x
+        q.copy_(b.dev16(x))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            g.replay()
+            first = out.clone()
+            step()
+            second = out.clone()
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, second) and torch.equal(first, out)
+        if i == 0:
+            b.oracle_append(freqs(64))
+        # the attention of the kernel's own rotated q and K, which have tests of
+        # their own
+        b.q = qr.double().cpu().numpy()
+        b.k, b.scales = b.gk.cpu().numpy(), b.gs.cpu().numpy()
+        ref = b.attention(0.125)
+        H.assert_attention_close(H.out_to_double(out), ref, "graph decode", W.BF16)
+        H.assert_attention_close(H.out_to_double(pre), ref, "graph prefill", W.BF16)
+    assert int(b.err.item()) == 0
+
+
 def test_decode_scaled_large_ratio_of_scales():
     """V of one block 2^12 larger than the others but with no weight (its keys
     point away): the small blocks keep their precision."""
