@@ -419,37 +419,63 @@ def pkv_block_hashes(token_ids, cu_seqlens, block_size, block_offsets=None, pare
 
 
 # ------------------------------------------------------------------ scaled cache
+#
+# A decode step's calls take a few microseconds on the GPU, as long as the
+# marshalling of their arguments: these functions look at each tensor once and
+# hand plain numbers to ctypes.
+
+_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
+_CODES = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
+
+
+def _current_stream(t, name, stream):
+    """The stream's handle; t must be on the current device, where a call runs."""
+    if _raw_stream is not None and _raw_device is not None:
+        i = _raw_device() if t.get_device() >= 0 else -2
+        if t.get_device() != i:
+            raise ValueError("%s must be on the current CUDA device" % name)
+        if stream is None:
+            return _raw_stream(i)
+    elif not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device" % name)
+    return _stream(stream)
+
 
 def _i32(t, name):
-    _dense(t, name)
-    if t.dtype != torch.int32:
-        raise ValueError("%s must be int32" % name)
-    return t
+    """Address of a dense int32 tensor."""
+    if t.dtype is not _I32 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous int32" % name)
+    return t.data_ptr()
 
 
 def _scales_of(cache, scales):
     """Device address of a layer's scales, float32 [num_blocks, num_kv_heads, 2]."""
-    _dense(scales, "scales")
-    if scales.dtype != torch.float32 or scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads:
-        raise ValueError("scales must be float32 [num_blocks, num_kv_heads, 2]")
+    if scales.dtype is not _F32 or not scales.is_contiguous() or \
+            scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads:
+        raise ValueError("scales must be contiguous float32 [num_blocks, num_kv_heads, 2]")
     return scales.data_ptr()
 
 
-def _on_device(t, name):
-    """A call runs on the current device; tensors of another are refused."""
-    i = t.get_device()
-    if i < 0 or i != (_raw_device() if _raw_device is not None else torch.cuda.current_device()):
-        raise ValueError("%s must be on the current CUDA device" % name)
+def _code16(t, name):
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError("%s must be float16 or bfloat16" % name)
+    return c
 
 
-def _token_rows(t, name):
-    """(tokens, heads, head_dim, elements between tokens) of t, whose heads lie
-    side by side (a slice of a fused projection will do)."""
-    n, h, d = t.shape
+def _token_rows(t, name, n, h, d):
+    """Elements between the tokens of t [n, h, d], whose heads lie side by side
+    (a slice of a fused projection will do)."""
     a, b, c = t.stride()
     if c != 1 or (h > 1 and b != d):
         raise ValueError("%s must be [tokens, heads, head_dim] with dense heads" % name)
-    return n, h, d, a if n > 1 else h * d
+    return a if n > 1 else h * d
+
+
+def _like(t, ref, name):
+    if t.shape != ref.shape or t.dtype is not ref.dtype or not t.is_contiguous():
+        raise ValueError("%s must be dense and like q" % name)
+    return t
 
 
 def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tables, context_lens,
@@ -459,40 +485,42 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     q (None without q).  `inv_freq` is a float64 device tensor of rot_dim / 2
     radians per position (rope.inv_freq computes it), or None to rotate
     nothing; with `scales` the cache is a scaled one."""
-    rows, kv, d, ks = _token_rows(k, "k")
-    rows_v, kv_v, d_v, vs = _token_rows(v, "v")
-    if kv != cache.num_kv_heads or d != cache.head_dim or (rows_v, kv_v, d_v) != (rows, kv, d) or \
-            v.dtype != k.dtype:
+    stream = _current_stream(k, "k", stream)
+    code = _code16(k, "k")
+    rows, kv, d = shape = k.shape
+    if kv != cache.num_kv_heads or d != cache.head_dim or v.shape != shape or \
+            v.dtype is not k.dtype:
         raise ValueError("k and v must be alike and fit the cache")
+    qp = qo = None
     qs = heads = 0
     if q is not None:
-        rows_q, heads, d_q, qs = _token_rows(q, "q")
-        if rows_q != rows or d_q != d or q.dtype != k.dtype:
+        rows_q, heads, d_q = q.shape
+        if rows_q != rows or d_q != d or q.dtype is not k.dtype:
             raise ValueError("q must have the tokens, head_dim and type of k")
+        qs = _token_rows(q, "q", rows, heads, d)
         if q_out is None:
-            q_out = torch.empty((rows, heads, d), dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
-            raise ValueError("q_out must be dense and like q")
-    rot = 0
+            q_out = torch.empty_like(q)        # (dense: q is, but for the space between tokens)
+        else:
+            _like(q_out, q, "q_out")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    rot, fp = 0, None
     if inv_freq is not None:
-        _dense(inv_freq, "inv_freq")
-        if inv_freq.dtype != torch.float64:
-            raise ValueError("inv_freq must be float64")
-        rot = 2 * inv_freq.numel()
+        if inv_freq.dtype is not _F64 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous float64")
+        rot, fp = 2 * inv_freq.numel(), inv_freq.data_ptr()
     num_seqs = context_lens.numel()
-    if cu_seqlens_q.numel() != num_seqs + 1:
-        raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
-    if block_tables.shape[0] != num_seqs:
-        raise ValueError("block_tables needs one row per sequence")
-    _on_device(k, "k")
-    _check(load().pkv_rope_append(
-        ctypes.byref(cache), _scales_of(cache, scales) if scales is not None else None,
-        q.data_ptr() if q is not None else None, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        dtype_code(k.dtype), heads, inv_freq.data_ptr() if rot else None, rot,
-        1 if interleaved else 0, mscale, num_seqs, _i32(cu_seqlens_q, "cu_seqlens_q").data_ptr(),
-        rows, max_q_len, _i32(block_tables, "block_tables").data_ptr(), block_tables.shape[1],
-        _i32(context_lens, "context_lens").data_ptr(), max_context_len, _ptr(dev_err),
-        q_out.data_ptr() if q is not None else None, _stream(stream)), "pkv_rope_append")
+    n_tables, width = block_tables.shape
+    if cu_seqlens_q.numel() != num_seqs + 1 or n_tables != num_seqs:
+        raise ValueError("cu_seqlens_q needs num_seqs + 1 entries, block_tables num_seqs rows")
+    st = (_lib or load()).pkv_rope_append(
+        ctypes.byref(cache), None if scales is None else _scales_of(cache, scales), qp, qs,
+        k.data_ptr(), _token_rows(k, "k", rows, kv, d), v.data_ptr(),
+        _token_rows(v, "v", rows, kv, d), code, heads, fp, rot, interleaved, mscale, num_seqs,
+        _i32(cu_seqlens_q, "cu_seqlens_q"), rows, max_q_len, _i32(block_tables, "block_tables"),
+        width, _i32(context_lens, "context_lens"), max_context_len,
+        None if dev_err is None else dev_err.data_ptr(), qo, stream)
+    if st:
+        raise PkvError(st, "pkv_rope_append")
     return q_out if q is not None else None
 
 
@@ -511,26 +539,26 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
                                       max_context_len, scale, partition_size=0, workspace=None,
                                       dev_err=None, out=None, stream=None):
     """Decode over a scaled cache; arguments as pkv_paged_attention_decode."""
-    _dense(q, "q")
+    stream = _current_stream(q, "q", stream)
     s, h, d = q.shape
-    if d != cache.head_dim or context_lens.numel() != s or block_tables.shape[0] != s:
-        raise ValueError("q, block_tables and context_lens do not fit together")
-    _on_device(q, "q")
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out must be dense and like q")
+    n_tables, width = block_tables.shape
+    if d != cache.head_dim or context_lens.numel() != s or n_tables != s or not q.is_contiguous():
+        raise ValueError("q (dense), block_tables and context_lens do not fit together")
+    out = torch.empty_like(q) if out is None else _like(out, q, "out")
+    wp, ws_bytes = None, 0
     if workspace is None:
         need = pkv_decode_scaled_workspace_bytes(cache, s, h, max_context_len, partition_size)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(load().pkv_paged_attention_decode_scaled(
-        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), dtype_code(q.dtype), s, h,
-        _i32(block_tables, "block_tables").data_ptr(), block_tables.shape[1],
-        _i32(context_lens, "context_lens").data_ptr(), max_context_len, scale, partition_size,
-        _ptr(workspace), ws_bytes, _ptr(dev_err), out.data_ptr(), _stream(stream)),
-        "pkv_paged_attention_decode_scaled")
+    if workspace is not None:
+        wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = (_lib or load()).pkv_paged_attention_decode_scaled(
+        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), s, h,
+        _i32(block_tables, "block_tables"), width, _i32(context_lens, "context_lens"),
+        max_context_len, scale, partition_size, wp, ws_bytes,
+        None if dev_err is None else dev_err.data_ptr(), out.data_ptr(), stream)
+    if st:
+        raise PkvError(st, "pkv_paged_attention_decode_scaled")
     return out
 
 
@@ -539,23 +567,22 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
                                        out=None, stream=None):
     """Causal attention over a scaled cache; arguments as
     pkv_paged_attention_prefill."""
-    _dense(q, "q")
+    stream = _current_stream(q, "q", stream)
     total, h, d = q.shape
     num_seqs = context_lens.numel()
-    if d != cache.head_dim or cu_seqlens_q.numel() != num_seqs + 1 or \
-            block_tables.shape[0] != num_seqs:
-        raise ValueError("q, cu_seqlens_q, block_tables and context_lens do not fit together")
-    _on_device(q, "q")
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out must be dense and like q")
-    _check(load().pkv_paged_attention_prefill_scaled(
-        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), dtype_code(q.dtype),
-        num_seqs, h, _i32(cu_seqlens_q, "cu_seqlens_q").data_ptr(), total, max_q_len,
-        _i32(block_tables, "block_tables").data_ptr(), block_tables.shape[1],
-        _i32(context_lens, "context_lens").data_ptr(), max_context_len, scale, _ptr(dev_err),
-        out.data_ptr(), _stream(stream)), "pkv_paged_attention_prefill_scaled")
+    n_tables, width = block_tables.shape
+    if d != cache.head_dim or cu_seqlens_q.numel() != num_seqs + 1 or n_tables != num_seqs or \
+            not q.is_contiguous():
+        raise ValueError("q (dense), cu_seqlens_q, block_tables and context_lens do not fit "
+                         "together")
+    out = torch.empty_like(q) if out is None else _like(out, q, "out")
+    st = (_lib or load()).pkv_paged_attention_prefill_scaled(
+        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), num_seqs, h,
+        _i32(cu_seqlens_q, "cu_seqlens_q"), total, max_q_len, _i32(block_tables, "block_tables"),
+        width, _i32(context_lens, "context_lens"), max_context_len, scale,
+        None if dev_err is None else dev_err.data_ptr(), out.data_ptr(), stream)
+    if st:
+        raise PkvError(st, "pkv_paged_attention_prefill_scaled")
     return out
 
 
@@ -571,9 +598,8 @@ def pkv_copy_blocks_scaled(caches, scales, block_pairs, dst=None, dst_scales=Non
     if len(scales) != n or (dst is None) != (dst_scales is None) or \
             (dst is not None and (len(dst) != n or len(dst_scales) != n)):
         raise ValueError("one array of scales per layer, and as many layers on both sides")
-    _dense(block_pairs, "block_pairs")
-    if block_pairs.dtype != torch.int64:
-        raise ValueError("block_pairs must be int64 [n, 2]")
+    if block_pairs.dtype is not torch.int64 or not block_pairs.is_contiguous():
+        raise ValueError("block_pairs must be contiguous int64 [n, 2]")
     ptrs = ctypes.c_void_p * n
     a = (CacheDesc * n)(*caches)
     a_s = ptrs(*[_scales_of(c, t) for c, t in zip(caches, scales)])
@@ -581,6 +607,11 @@ def pkv_copy_blocks_scaled(caches, scales, block_pairs, dst=None, dst_scales=Non
     if dst is not None:
         b = (CacheDesc * n)(*dst)
         b_s = ptrs(*[_scales_of(c, t) for c, t in zip(dst, dst_scales)])
-    _check(load().pkv_copy_blocks_scaled(a, a_s, b, b_s, n, _ptr(block_pairs),
-                                         block_pairs.numel() // 2, _ptr(dev_err),
-                                         _stream(stream)), "pkv_copy_blocks_scaled")
+        stream = _stream(stream)
+    else:
+        stream = _current_stream(block_pairs, "block_pairs", stream)
+    st = (_lib or load()).pkv_copy_blocks_scaled(
+        a, a_s, b, b_s, n, block_pairs.data_ptr(), block_pairs.numel() // 2,
+        None if dev_err is None else dev_err.data_ptr(), stream)
+    if st:
+        raise PkvError(st, "pkv_copy_blocks_scaled")
