@@ -561,38 +561,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         // ---------------- load and convert (four warps) ----------------
-        constexpr int VPR = D / 16;                // 16-code vectors per row
-        constexpr int RPI = 32 / VPR;              // rows per warp access
-        constexpr int NV = kKeys / (RPI * kConvWarps);   // vectors a lane holds of a tile
+        // A lane's vector i (16 codes) of a tile: row group i / NP (32 rows: 8 to a
+        // warp), 64-dim panel i % NP, row `rsub` and quarter `c4` of the panel's
+        // row.  Eight lanes write two rows' chunks of one parity, which the
+        // swizzle sends to eight different banks.
+        constexpr int NP = L::NP;
+        constexpr int NV = NP * 4;
+        static_assert(NV % kBatch == 0, "whole batches");
         const int cw = warp - kConvWarp;
-        const int c16 = lane % VPR;
-        const int rsub = cw * RPI + lane / VPR;    // row of the lane's vector 0
-        // D = 128: lanes of the second 64-dim panel store their halves in the
-        // other order, so that eight lanes never meet in a bank
-        const int flip = D == 128 ? c16 >> 2 : 0;
+        const int c4 = lane & 3;
+        const int rsub = cw * 8 + (lane >> 2);
         const int64_t tile_bytes = (int64_t)BS * D;
         const unsigned char* kbase = reinterpret_cast<const unsigned char*>(p.k_cache) + g * tile_bytes;
         const unsigned char* vbase = reinterpret_cast<const unsigned char*>(p.v_cache) + g * tile_bytes;
         const int64_t stride = p.num_kv_heads * tile_bytes;
-        // lane i < NB: block i of a K/V tile: its id (-1: none) and its factors
-        struct Entry {
-            int phys;
-            uint32_t fk, fv;
-        };
-        auto entry = [&](int kt) -> Entry {
-            Entry e{-1, 0u, 0u};
+        // lane i < NB: block i of a K/V tile: its id (-1: none), its factors.  The
+        // id is asked for three tiles ahead, the scales two, so that neither
+        // load is waited for.
+        auto id_of = [&](int kt) -> int {
             const int tok = kt * kKeys + lane * BS;
-            if (lane < NB && tok < kv_end) {
-                const int phys = __ldg(table + tok / BS);
-                if (phys >= 0 && (int64_t)phys < p.num_blocks) {
-                    const float2 sc = __ldg(scales + (int64_t)phys * p.num_kv_heads + g);
-                    e.phys = phys;
-                    const float fk = sc.x / kref * kUnit, fv = sc.y / vref * kUnit;
-                    e.fk = pack_rn<kF16>(fk, fk);
-                    e.fv = pack_rn<kF16>(fv, fv);
-                }
-            }
-            return e;
+            return kt < nk && lane < NB && tok < kv_end ? __ldg(table + tok / BS) : -1;
+        };
+        auto good = [&](int phys) { return phys >= 0 && (int64_t)phys < p.num_blocks; };
+        auto scales_of = [&](int phys) -> float2 {
+            return good(phys) ? __ldg(scales + (int64_t)phys * p.num_kv_heads + g) : make_float2(0.f, 0.f);
+        };
+        auto factor = [&](float sc, float ref) -> uint32_t {
+            const float f = sc / ref * kUnit;
+            return pack_rn<kF16>(f, f);
         };
         // Codes travel through a staging area in which every thread has places of
         // its own (vector i at i * 128 + thread): copied asynchronously one slot
@@ -601,71 +597,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t raw_k = sb + L::raw + (tid - kConvWarp * 32) * 16;
         const uint32_t raw_v = raw_k + kKeys * D;
         constexpr int PITCH = 32 * kConvWarps * 16;
-        // start the copy of vector i of a tile whose first key is `first`
-        auto fetch = [&](uint32_t dst, const unsigned char* base, const Entry& e, int i, int first,
-                         int end) {
-            const int row = i * RPI * kConvWarps + rsub;
-            const int phys = __shfl_sync(0xffffffffu, e.phys, row / BS);
-            const bool ok = phys >= 0 && first + row < end;
-            cp16z(dst + i * PITCH,
-                  base + (ok ? (int64_t)phys * stride + (row % BS) * D + c16 * 16 : 0), ok);
-        };
-        // convert vectors i0 ... i0 + kBatch - 1, with their blocks' factors, into
-        // their places of an operand tile; a batch's reads, conversions and
-        // writes stand together, since one warp per scheduler has nothing but
-        // its own independent instructions to hide their latency
-        auto factors = [&](uint32_t f, int i0, uint32_t(&fi)[kBatch]) {
+        // start the copies of vectors i0 ... of a tile whose first key is `first`
+        auto fetch = [&](uint32_t dst, const unsigned char* base, int id, int i0, int first, int end) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                fi[u] = __shfl_sync(0xffffffffu, f, ((i0 + u) * RPI * kConvWarps + rsub) / BS);
-        };
-        auto store = [&](uint32_t dst, const uint32_t(&fi)[kBatch], int i0, const uint4(&x)[kBatch]) {
-            uint4 lo[kBatch], hi[kBatch];
+            for (int u = 0; u < kBatch; u += NP) {
+                const int row = (i0 + u) / NP * 32 + rsub;
+                const int phys = __shfl_sync(0xffffffffu, id, row / BS);
+                const bool ok = good(phys) && first + row < end;
+                const unsigned char* src = base + (ok ? phys * stride + (row % BS) * D + c4 * 16 : 0);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                convert16(x[u], fi[u], lo[u], hi[u]);
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int row = (i0 + u) * RPI * kConvWarps + rsub;
-                st_shared16(dst + panel_off(row, 2 * c16 + flip, kKeys), flip ? hi[u] : lo[u]);
-                st_shared16(dst + panel_off(row, 2 * c16 + (flip ^ 1), kKeys), flip ? lo[u] : hi[u]);
+                for (int q = 0; q < NP; ++q)
+                    cp16z(dst + (i0 + u + q) * PITCH, src + q * 64, ok);
             }
         };
-        Entry prev{-1, 0u, 0u}, cur = entry(0), next = nk > 1 ? entry(1) : prev;
+        // convert vectors i0 ..., with their blocks' factors, into their places of
+        // an operand tile; a batch's reads, conversions and writes stand
+        // together, since one warp per scheduler has nothing but its own
+        // independent instructions to hide their latency
+        const uint32_t place = panel_off(rsub, 2 * c4, kKeys);
+        const uint32_t place1 = panel_off(rsub, 2 * c4 + 1, kKeys);
+        auto store = [&](uint32_t dst, uint32_t f, int i0, const uint4(&x)[kBatch]) {
+            uint4 lo[kBatch], hi[kBatch];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            fetch(raw_k, kbase, cur, i, 0, kv_end);
+            for (int u = 0; u < kBatch; u += NP) {
+                const uint32_t fi = __shfl_sync(0xffffffffu, f, ((i0 + u) / NP * 32 + rsub) / BS);
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+                    convert16(x[u + q], fi, lo[u + q], hi[u + q]);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t at = (i0 + u) / NP * 32 * 128 + (i0 + u) % NP * kKeys * 128;
+                st_shared16(dst + place + at, lo[u]);
+                st_shared16(dst + place1 + at, hi[u]);
+            }
+        };
+        int id0 = id_of(0), id1 = id_of(1), id2 = id_of(2);      // tiles j, j + 1, j + 2
+        float2 sc0 = scales_of(id0), sc1 = scales_of(id1);
+        uint32_t fv = 0u;                                          // V's factor of tile j - 1
+#pragma unroll
+        for (int i0 = 0; i0 < NV; i0 += kBatch)
+            fetch(raw_k, kbase, id0, i0, 0, kv_end);
         cp_async_commit();
         for (int j = 0; j <= nk; ++j) {
             const int st = j % ST;
-            const Entry after = j + 2 < nk ? entry(j + 2) : Entry{-1, 0u, 0u};
+            const int id3 = id_of(j + 3);
+            const float2 sc2 = scales_of(id2);
+            const uint32_t fk = factor(sc0.x, kref);
             cp_async_wait<0>();
             if (!wait_warp(s_addr(&bars.empty[st]), ((j / ST) & 1) ^ 1, &abort_flag, p.dev_err))
                 break;
             const uint32_t dst = sb + L::slot + st * L::SLOT;
             // each place is refilled for the next slot once its codes are used
+            if (j < nk) {
 #pragma unroll
-            for (int i0 = 0; i0 < NV; i0 += kBatch) {
-                if (j < nk) {
-                    uint32_t fi[kBatch];
+                for (int i0 = 0; i0 < NV; i0 += kBatch) {
                     uint4 x[kBatch];
-                    factors(cur.fk, i0, fi);
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u)
                         x[u] = lds16(raw_k + (i0 + u) * PITCH);
-                    store(dst, fi, i0, x);
+                    store(dst, fk, i0, x);
                     if (j + 1 < nk)
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u)
-                            fetch(raw_k, kbase, next, i0 + u, (j + 1) * kKeys, kv_end);
+                        fetch(raw_k, kbase, id1, i0, (j + 1) * kKeys, kv_end);
                 }
             }
 #pragma unroll
             for (int i0 = 0; i0 < NV; i0 += kBatch) {
                 if (j > 0) {
-                    uint32_t fi[kBatch];
                     uint4 x[kBatch];
-                    factors(prev.fv, i0, fi);
                     uint32_t bad = 0;
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
@@ -677,30 +676,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // NaN codes: 0 in the tile, the position noted
 #pragma unroll
                         for (int u = 0; u < kBatch; ++u) {
+                            const int row = (i0 + u) / NP * 32 + rsub;
+                            int* col = nan_pos + (i0 + u) % NP * 64 + c4 * 16;
                             uint32_t w4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
                             for (int q4 = 0; q4 < 4; ++q4)
-                                w4[q4] = note_nans(w4[q4], nan_pos + c16 * 16 + q4 * 4, &any_nan,
-                                                   (j - 1) * kKeys + (i0 + u) * RPI * kConvWarps + rsub);
+                                w4[q4] = note_nans(w4[q4], col + q4 * 4, &any_nan, (j - 1) * kKeys + row);
                             x[u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
                         }
                     }
                     __syncwarp();
-                    store(dst + L::KVB, fi, i0, x);
+                    store(dst + L::KVB, fv, i0, x);
                 }
                 if (j < nk)
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u)
-                        fetch(raw_v, vbase, cur, i0 + u, j * kKeys, kv_end);
+                    fetch(raw_v, vbase, id0, i0, j * kKeys, kv_end);
             }
             cp_async_commit();
             async_proxy_fence();
             __syncwarp();
             if (lane == 0)
                 bar_arrive(s_addr(&bars.full[st]));
-            prev = cur;
-            cur = next;
-            next = after;
+            fv = factor(sc0.y, vref);
+            id0 = id1;
+            id1 = id2;
+            id2 = id3;
+            sc0 = sc1;
+            sc1 = sc2;
         }
         cp_async_wait<0>();
     }
