@@ -586,8 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto scales_of = [&](int phys) -> float2 {
             return good(phys) ? __ldg(scales + (int64_t)phys * p.num_kv_heads + g) : make_float2(0.f, 0.f);
         };
-        auto factor = [&](float sc, float ref) -> uint32_t {
-            const float f = sc / ref * kUnit;
+        // (the references are powers of two: their inverses are exact)
+        const float kinv = 1.f / kref, vinv = 1.f / vref;
+        auto factor = [&](float sc, float inv) -> uint32_t {
+            const float f = sc * inv * kUnit;
             return pack_rn<kF16>(f, f);
         };
         // Codes travel through a staging area in which every thread has places of
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = j % ST;
             const int id3 = id_of(j + 3);
             const float2 sc2 = scales_of(id2);
-            const uint32_t fk = factor(sc0.x, kref);
+            const uint32_t fk = factor(sc0.x, kinv);
             cp_async_wait<0>();
             if (!wait_warp(s_addr(&bars.empty[st]), ((j / ST) & 1) ^ 1, &abort_flag, p.dev_err))
                 break;
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0)
                 bar_arrive(s_addr(&bars.full[st]));
-            fv = factor(sc0.y, vref);
+            fv = factor(sc0.y, vinv);
             id0 = id1;
             id1 = id2;
             id2 = id3;
