@@ -73,7 +73,8 @@ template <int ST>
 struct Bars {
     uint64_t q_full[2];      // 128 arrivals: the group's Q rows are in shared memory
     uint64_t s_full[2];      // commit: S_w(kt) (and every earlier product of w) done
-    uint64_t p_full[2];      // 128 arrivals: P_w(kt) written
+    uint64_t p_most[2];      // 128 arrivals: three quarters of P_w(kt) written
+    uint64_t p_full[2];      // 128 arrivals: all of it
     uint64_t o_full[2];      // commit: the last O_w += P_w V done
     uint64_t full[ST];       // one arrival per converting warp: slot j is stored
     uint64_t empty[ST];      // one arrival per issuing warp: slot j no longer read
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < 2; ++w) {
             bar_init(s_addr(&bars.q_full[w]), kRows);
             bar_init(s_addr(&bars.s_full[w]), 1);
+            bar_init(s_addr(&bars.p_most[w]), kRows);
             bar_init(s_addr(&bars.p_full[w]), kRows);
             bar_init(s_addr(&bars.o_full[w]), 1);
         }
@@ -452,6 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hi[e] = pack_rn<kF16>(pp.x, pp.y);
                     }
                     tmem_st8(t_s + c0, hi);
+                    if (c0 + 16 == kKeys / 4 * 3) {
+                        // the product may start on the first three quarters
+                        tmem_wait_st();
+                        tc_fence_before();
+                        bar_arrive(s_addr(&bars.p_most[w]));
+                    }
                 }
                 const float lsum = ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) +
                                    ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
@@ -517,20 +525,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_one(s_addr(&bars.full[j % ST]), (j / ST) & 1, &abort_flag, p.dev_err))
                     break;
                 const bool pv = j > 0 && j <= nkv;
-                if (pv && !wait_one(s_addr(&bars.p_full[w]), (j - 1) & 1, &abort_flag, p.dev_err))
-                    break;
+                // (the weights last: they are the ones that come late, and every
+                // wait that has to be looked at costs a few hundred cycles)
                 if (w == 1 ? !wait_one(s_addr(&bars.issued[0]), j & 1, &abort_flag, p.dev_err)
                            : (ntok1 > 0 && j > 0 &&
                               !wait_one(s_addr(&bars.issued[1]), (j - 1) & 1, &abort_flag, p.dev_err)))
+                    break;
+                if (pv && !wait_one(s_addr(&bars.p_most[w]), (j - 1) & 1, &abort_flag, p.dev_err))
                     break;
                 bool used = false;
                 if (pv) {
                     tc_fence_after();
                     const uint32_t acc0 = j > 1 ? 1u : 0u;
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                    for (int ks = 0; ks < kKeys / 64 * 3; ++ks)
                         umma_ts_h(o_col, s_col + ks * 16, v_lo + sl + (uint32_t)(ks * 16 * 128 >> 4),
                                   hi1k, id_o, ks > 0 ? 1u : acc0);
+                    if (!wait_one(s_addr(&bars.p_full[w]), (j - 1) & 1, &abort_flag, p.dev_err))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = kKeys / 64 * 3; ks < kKeys / 16; ++ks)
+                        umma_ts_h(o_col, s_col + ks * 16, v_lo + sl + (uint32_t)(ks * 16 * 128 >> 4),
+                                  hi1k, id_o, 1u);
                     if (j == nkv)
                         umma_commit(s_addr(&bars.o_full[w]));
                     used = true;
