@@ -158,6 +158,18 @@ __device__ __forceinline__ void convert16(const uint4& c, uint32_t f, uint4& lo,
     hi.z = mul(a), hi.w = mul(b);
 }
 
+// Larger magnitudes of two words of 16-bit values (NaN gives way to a number).
+template <int T>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (T == kBF16)
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+    else
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+    return r;
+}
+
 // Non-zero where a byte of w is a NaN code (0x7f or 0xff).
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w)
 {
@@ -339,45 +351,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int jw = j0 + w * QT;
             const int pos0 = w ? pos01 : pos00;
             const int nkv = w ? nkv1 : nkv0;
+            // q in fp16, scaled per row to at most 2^14 in size; rows past the
+            // tile's are zero.  The warp copies its 32 rows side by side into
+            // their places, then every thread turns its own row into fp16 there.
+            // (Loops kept short: code that runs once is fetched at a few bytes
+            // a cycle; the same unrolled took 11,000 cycles.)
+            constexpr int LPR = D / 8;                 // lanes to a row
+            constexpr int RPA = 32 / LPR;              // rows to an access
+            constexpr int NA = 32 / RPA;               // accesses
+            // offset of row rr of the tile from its first: rr / G tokens on, by a
+            // multiplication (exact: 128 rows, G <= 128)
+            const uint32_t by_g = ((1u << 24) + G - 1) / G;
+            const int64_t first = row_off(jw, 0);
+            auto row_at = [&](int rr) -> int64_t {
+                return (int64_t)((rr * by_g) >> 24) * ((p.num_heads - G) * D) + rr * D;
+            };
+            const uint32_t qs = sb + L::q + w * L::QB;
+            const int row0 = (warp & 3) * 32;
             float qk;                                  // this row's factor of the scores
             {
-                // q in fp16, scaled to at most 2^14 in size; rows past the
-                // tile's are zero
-                const uint32_t qs = sb + L::q + w * L::QB;
-                const bool ok = r < nrows;
-                const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) +
-                                      (ok ? row_off(jw + r / G, r % G) : 0);
-                float up = 1.f;
-                uint4 v[D / 8];
-                float mx = 0.f;
-#pragma unroll
+                const int c0 = lane % LPR;
+#pragma unroll 4
+                for (int i = 0; i < NA; ++i) {
+                    const int rr = row0 + i * RPA + lane / LPR;
+                    const bool ok = rr < nrows;
+                    cp16z(qs + panel_off(rr, c0, kRows),
+                          reinterpret_cast<const uint16_t*>(p.q) + (ok ? first + row_at(rr) + c0 * 8 : 0),
+                          ok);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                __syncwarp();
+                uint32_t m2 = 0u;
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    v[c] = ok ? ld_ro(src + c * 8) : make_uint4(0, 0, 0, 0);
-                    float x[8];
-                    unpack_vec<CT>(v[c], x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        mx = fmaxf(mx, fabsf(x[e]));
+                    const uint4 v = lds16(qs + panel_off(r, c, kRows));
+                    m2 = max_abs2<CT>(max_abs2<CT>(m2, v.x), v.y);
+                    m2 = max_abs2<CT>(max_abs2<CT>(m2, v.z), v.w);
                 }
-                if (mx > 0.f && mx < __builtin_huge_valf()) {
-                    const float ex = 13.f - (float)((int)(__float_as_uint(mx) >> 23) - 127);
-                    up = exp2f(fminf(fmaxf(ex, -120.f), 120.f));
-                }
-                // the factor of the scores stays positive: the scale's sign (or
-                // a scale of 0) goes into q
+                const float2 mm = unpack2<CT>(m2);
+                const float mx = fmaxf(mm.x, mm.y);
+                // 2^13 / 2^floor(log2 mx), kept where it and its inverse are normal
+                float up = 1.f;
+                if (mx > 0.f && mx < __builtin_huge_valf())
+                    up = __uint_as_float(
+                        (uint32_t)min(max(267 - (int)(__float_as_uint(mx) >> 23), 7), 247) << 23);
+                // the factor of the scores stays positive: the scale's sign (or a
+                // scale of 0) goes into q
                 const float sign = p.qk_scale_log2 < 0.f ? -1.f : (p.qk_scale_log2 == 0.f ? 0.f : 1.f);
                 qk = sign == 0.f ? 1.f
                                  : fabsf(p.qk_scale_log2) * (1.f / up) * (kref * (1.f / kUnit));
                 up *= sign;
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    float x[8];
-                    unpack_vec<CT>(v[c], x);
-                    st_shared16(qs + panel_off(r, c, kRows),
-                                make_uint4(pack_rn<kF16>(x[0] * up, x[1] * up),
-                                           pack_rn<kF16>(x[2] * up, x[3] * up),
-                                           pack_rn<kF16>(x[4] * up, x[5] * up),
-                                           pack_rn<kF16>(x[6] * up, x[7] * up)));
+                    const uint32_t at = qs + panel_off(r, c, kRows);
+                    const uint4 v = lds16(at);
+                    const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = unpack2<CT>(w4[e]);
+                        h[e] = pack_rn<kF16>(x.x * up, x.y * up);
+                    }
+                    st_shared16(at, make_uint4(h[0], h[1], h[2], h[3]));
                 }
                 async_proxy_fence();
                 bar_arrive(s_addr(&bars.q_full[w]));
@@ -476,27 +512,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = l_run > 0.f ? (1.f / l_run) * (vref * (1.f / kUnit))
                                               : (l_run == 0.f ? 0.f : l_run);
                 const bool nans = *reinterpret_cast<volatile int*>(&any_nan) != 0;
+                // through shared memory (this tile's q, which every product has
+                // read), so that the warp writes its rows side by side
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 16) {
-                    uint32_t r16[16];
-                    tmem_ld16(t_o + c0, r16);
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o32[32];
+                    tmem_ld16(t_o + c0, *reinterpret_cast<uint32_t(*)[16]>(o32));
+                    tmem_ld16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(o32 + 16));
                     tmem_wait_ld();
                     if (nans) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
+                        for (int e = 0; e < 32; ++e)
                             if (*reinterpret_cast<volatile int*>(&nan_pos[c0 + e]) <= pos)
-                                r16[e] = 0x7fffffffu;
+                                o32[e] = 0x7fffffffu;
                     }
-                    if (r < nrows) {
-                        uint32_t o8[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o8[e] = pack2(round_to<CT>(__uint_as_float(r16[2 * e]) * inv),
-                                          round_to<CT>(__uint_as_float(r16[2 * e + 1]) * inv));
-                        uint16_t* dst = out + row_off(jw + r / G, r % G) + c0;
-                        st_v4(dst, make_uint4(o8[0], o8[1], o8[2], o8[3]));
-                        st_v4(dst + 8, make_uint4(o8[4], o8[5], o8[6], o8[7]));
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o4[e] = pack_rn<CT>(__uint_as_float(o32[8 * c + 2 * e]) * inv,
+                                                __uint_as_float(o32[8 * c + 2 * e + 1]) * inv);
+                        st_shared16(qs + panel_off(r, c0 / 8 + c, kRows),
+                                    make_uint4(o4[0], o4[1], o4[2], o4[3]));
                     }
+                }
+                __syncwarp();
+                const int c = lane % LPR;
+#pragma unroll 4
+                for (int i = 0; i < NA; ++i) {
+                    const int rr = row0 + i * RPA + lane / LPR;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(qs + panel_off(rr, c, kRows))
+                                 : "memory");
+                    if (rr < nrows)
+                        st_v4(out + first + row_at(rr) + c * 8, v);
                 }
             }
         }
