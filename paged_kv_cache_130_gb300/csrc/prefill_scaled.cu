@@ -158,15 +158,11 @@ __device__ __forceinline__ void convert16(const uint4& c, uint32_t f, uint4& lo,
     hi.z = mul(a), hi.w = mul(b);
 }
 
-// Larger magnitudes of two words of 16-bit values (NaN gives way to a number).
-template <int T>
+// Larger magnitudes of two words of bf16 values (NaN gives way to a number).
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    if constexpr (T == kBF16)
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
-    else
-        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
     return r;
 }
 
@@ -310,6 +306,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     __syncthreads();
+    // ---------------- what can start before the scales are known ----------------
+    // Softmax warps: q, in its own type.  A warp copies its 32 rows side by side
+    // into their places; rows past the tile's are zero.
+    constexpr int LPR = D / 8;                 // lanes to a row
+    constexpr int RPA = 32 / LPR;              // rows to an access
+    constexpr int NA = 32 / RPA;               // accesses
+    const int qw = (warp >> 2) & 1;            // the warp's query tile
+    const int nrows = (qw ? ntok1 : ntok0) * G;
+    const int row0 = (warp & 3) * 32;
+    const uint32_t qs = sb + L::q + qw * L::QB;
+    // offset of row rr of the tile from its first: rr / G tokens on, by a
+    // multiplication (exact: 128 rows, G <= 128)
+    const uint32_t by_g = ((1u << 24) + G - 1) / G;
+    const int64_t first_row = row_off(j0 + qw * QT, 0);
+    auto row_at = [&](int rr) -> int64_t {
+        return (int64_t)((rr * by_g) >> 24) * ((p.num_heads - G) * D) + rr * D;
+    };
+    if (warp < 8 && nrows > 0) {
+        const int c = lane % LPR;
+#pragma unroll 4
+        for (int i = 0; i < NA; ++i) {
+            const int rr = row0 + i * RPA + lane / LPR;
+            const bool ok = rr < nrows;
+            cp16z(qs + panel_off(rr, c, kRows),
+                  reinterpret_cast<const uint16_t*>(p.q) + (ok ? first_row + row_at(rr) + c * 8 : 0), ok);
+        }
+        cp_async_commit();
+    }
+    // Converting warps: the first tile's codes.
+    // A lane's vector i (16 codes) of a tile: row group i / NP (32 rows: 8 to a
+    // warp), 64-dim panel i % NP, row `rsub` and quarter `c4` of the panel's
+    // row.  Eight lanes write two rows' chunks of one parity, which the
+    // swizzle sends to eight different banks.
+    constexpr int NP = L::NP;
+    constexpr int NV = NP * 4;
+    static_assert(NV % kBatch == 0, "whole batches");
+    const int cw = warp - kConvWarp;
+    const int c4 = lane & 3;
+    const int rsub = cw * 8 + (lane >> 2);
+    const int64_t tile_bytes = (int64_t)BS * D;
+    const unsigned char* kbase = reinterpret_cast<const unsigned char*>(p.k_cache) + g * tile_bytes;
+    const unsigned char* vbase = reinterpret_cast<const unsigned char*>(p.v_cache) + g * tile_bytes;
+    const int64_t stride = p.num_kv_heads * tile_bytes;
+    // lane i < NB: block i of a K/V tile: its id (-1: none), its factors.  The
+    // id is asked for three tiles ahead, the scales two, so that neither
+    // load is waited for.
+    auto id_of = [&](int kt) -> int {
+        const int tok = kt * kKeys + lane * BS;
+        return kt < nk && lane < NB && tok < kv_end ? __ldg(table + tok / BS) : -1;
+    };
+    auto good = [&](int phys) { return phys >= 0 && (int64_t)phys < p.num_blocks; };
+    // Codes travel through a staging area in which every thread has places of
+    // its own (vector i at i * 128 + thread): copied asynchronously one slot
+    // ahead, read back and converted by the thread that asked for them, so
+    // no barrier stands between.
+    const uint32_t raw_k = sb + L::raw + (tid - kConvWarp * 32) * 16;
+    const uint32_t raw_v = raw_k + kKeys * D;
+    constexpr int PITCH = 32 * kConvWarps * 16;
+    // start the copies of vectors i0 ... of a tile whose first key is `first`
+    auto fetch = [&](uint32_t dst, const unsigned char* base, int id, int i0, int first, int end) {
+#pragma unroll
+        for (int u = 0; u < kBatch; u += NP) {
+            const int row = (i0 + u) / NP * 32 + rsub;
+            const int phys = __shfl_sync(0xffffffffu, id, row / BS);
+            const bool ok = good(phys) && first + row < end;
+            const unsigned char* src = base + (ok ? phys * stride + (row % BS) * D + c4 * 16 : 0);
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+                cp16z(dst + (i0 + u + q) * PITCH, src + q * 64, ok);
+        }
+    };
+    int id0 = -1, id1 = -1, id2 = -1;          // tiles j, j + 1, j + 2
+    if (warp >= kConvWarp) {
+        id0 = id_of(0);
+        id1 = id_of(1);
+        id2 = id_of(2);
+#pragma unroll
+        for (int i0 = 0; i0 < NV; i0 += kBatch)
+            fetch(raw_k, kbase, id0, i0, 0, kv_end);
+        cp_async_commit();
+    }
     // the largest scales of the CTA's blocks
     {
         uint32_t mk = 0, mv = 0;
@@ -343,54 +420,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 8) {
         // ---------------- softmax of query tile w ----------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        const int w = warp >> 2;
+        const int w = qw;
         const int r = tid & (kRows - 1);
-        const int ntok = w ? ntok1 : ntok0;
-        if (ntok > 0) {
-            const int nrows = ntok * G;
-            const int jw = j0 + w * QT;
+        if (nrows > 0) {
             const int pos0 = w ? pos01 : pos00;
             const int nkv = w ? nkv1 : nkv0;
-            // q in fp16, scaled per row to at most 2^14 in size; rows past the
-            // tile's are zero.  The warp copies its 32 rows side by side into
-            // their places, then every thread turns its own row into fp16 there.
-            // (Loops kept short: code that runs once is fetched at a few bytes
-            // a cycle; the same unrolled took 11,000 cycles.)
-            constexpr int LPR = D / 8;                 // lanes to a row
-            constexpr int RPA = 32 / LPR;              // rows to an access
-            constexpr int NA = 32 / RPA;               // accesses
-            // offset of row rr of the tile from its first: rr / G tokens on, by a
-            // multiplication (exact: 128 rows, G <= 128)
-            const uint32_t by_g = ((1u << 24) + G - 1) / G;
-            const int64_t first = row_off(jw, 0);
-            auto row_at = [&](int rr) -> int64_t {
-                return (int64_t)((rr * by_g) >> 24) * ((p.num_heads - G) * D) + rr * D;
-            };
-            const uint32_t qs = sb + L::q + w * L::QB;
-            const int row0 = (warp & 3) * 32;
+            // fp16 q takes part as it is; bf16 q is scaled per row to at most 2^14
+            // in size, every thread turning its own row into fp16 in place.
+            // (Loops kept short: code that runs once is fetched at a few bytes a
+            // cycle; all of this unrolled took 11,000 cycles.)
             float qk;                                  // this row's factor of the scores
             {
-                const int c0 = lane % LPR;
-#pragma unroll 4
-                for (int i = 0; i < NA; ++i) {
-                    const int rr = row0 + i * RPA + lane / LPR;
-                    const bool ok = rr < nrows;
-                    cp16z(qs + panel_off(rr, c0, kRows),
-                          reinterpret_cast<const uint16_t*>(p.q) + (ok ? first + row_at(rr) + c0 * 8 : 0),
-                          ok);
-                }
-                cp_async_commit();
                 cp_async_wait<0>();
                 __syncwarp();
-                uint32_t m2 = 0u;
+                float mx = 0.f;
+                if constexpr (CT == kBF16) {
+                    uint32_t m2 = 0u;
 #pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = lds16(qs + panel_off(r, c, kRows));
-                    m2 = max_abs2<CT>(max_abs2<CT>(m2, v.x), v.y);
-                    m2 = max_abs2<CT>(max_abs2<CT>(m2, v.z), v.w);
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 v = lds16(qs + panel_off(r, c, kRows));
+                        m2 = max_abs2(max_abs2(m2, v.x), v.y);
+                        m2 = max_abs2(max_abs2(m2, v.z), v.w);
+                    }
+                    const float2 mm = unpack2<CT>(m2);
+                    mx = fmaxf(mm.x, mm.y);
                 }
-                const float2 mm = unpack2<CT>(m2);
-                const float mx = fmaxf(mm.x, mm.y);
                 // 2^13 / 2^floor(log2 mx), kept where it and its inverse are normal
                 float up = 1.f;
                 if (mx > 0.f && mx < __builtin_huge_valf())
@@ -402,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 qk = sign == 0.f ? 1.f
                                  : fabsf(p.qk_scale_log2) * (1.f / up) * (kref * (1.f / kUnit));
                 up *= sign;
+                if (up != 1.f || CT == kBF16)
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     const uint32_t at = qs + panel_off(r, c, kRows);
@@ -548,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : "r"(qs + panel_off(rr, c, kRows))
                                  : "memory");
                     if (rr < nrows)
-                        st_v4(out + first + row_at(rr) + c * 8, v);
+                        st_v4(out + first_row + row_at(rr) + c * 8, v);
                 }
             }
         }
@@ -630,28 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         // ---------------- load and convert (four warps) ----------------
-        // A lane's vector i (16 codes) of a tile: row group i / NP (32 rows: 8 to a
-        // warp), 64-dim panel i % NP, row `rsub` and quarter `c4` of the panel's
-        // row.  Eight lanes write two rows' chunks of one parity, which the
-        // swizzle sends to eight different banks.
-        constexpr int NP = L::NP;
-        constexpr int NV = NP * 4;
-        static_assert(NV % kBatch == 0, "whole batches");
-        const int cw = warp - kConvWarp;
-        const int c4 = lane & 3;
-        const int rsub = cw * 8 + (lane >> 2);
-        const int64_t tile_bytes = (int64_t)BS * D;
-        const unsigned char* kbase = reinterpret_cast<const unsigned char*>(p.k_cache) + g * tile_bytes;
-        const unsigned char* vbase = reinterpret_cast<const unsigned char*>(p.v_cache) + g * tile_bytes;
-        const int64_t stride = p.num_kv_heads * tile_bytes;
-        // lane i < NB: block i of a K/V tile: its id (-1: none), its factors.  The
-        // id is asked for three tiles ahead, the scales two, so that neither
-        // load is waited for.
-        auto id_of = [&](int kt) -> int {
-            const int tok = kt * kKeys + lane * BS;
-            return kt < nk && lane < NB && tok < kv_end ? __ldg(table + tok / BS) : -1;
-        };
-        auto good = [&](int phys) { return phys >= 0 && (int64_t)phys < p.num_blocks; };
         auto scales_of = [&](int phys) -> float2 {
             return good(phys) ? __ldg(scales + (int64_t)phys * p.num_kv_heads + g) : make_float2(0.f, 0.f);
         };
@@ -660,26 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto factor = [&](float sc, float inv) -> uint32_t {
             const float f = sc * inv * kUnit;
             return pack_rn<kF16>(f, f);
-        };
-        // Codes travel through a staging area in which every thread has places of
-        // its own (vector i at i * 128 + thread): copied asynchronously one slot
-        // ahead, read back and converted by the thread that asked for them, so
-        // no barrier stands between.
-        const uint32_t raw_k = sb + L::raw + (tid - kConvWarp * 32) * 16;
-        const uint32_t raw_v = raw_k + kKeys * D;
-        constexpr int PITCH = 32 * kConvWarps * 16;
-        // start the copies of vectors i0 ... of a tile whose first key is `first`
-        auto fetch = [&](uint32_t dst, const unsigned char* base, int id, int i0, int first, int end) {
-#pragma unroll
-            for (int u = 0; u < kBatch; u += NP) {
-                const int row = (i0 + u) / NP * 32 + rsub;
-                const int phys = __shfl_sync(0xffffffffu, id, row / BS);
-                const bool ok = good(phys) && first + row < end;
-                const unsigned char* src = base + (ok ? phys * stride + (row % BS) * D + c4 * 16 : 0);
-#pragma unroll
-                for (int q = 0; q < NP; ++q)
-                    cp16z(dst + (i0 + u + q) * PITCH, src + q * 64, ok);
-            }
         };
         // convert vectors i0 ..., with their blocks' factors, into their places of
         // an operand tile; a batch's reads, conversions and writes stand
@@ -703,13 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared16(dst + place1 + at, hi[u]);
             }
         };
-        int id0 = id_of(0), id1 = id_of(1), id2 = id_of(2);      // tiles j, j + 1, j + 2
         float2 sc0 = scales_of(id0), sc1 = scales_of(id1);
         uint32_t fv = 0u;                                          // V's factor of tile j - 1
-#pragma unroll
-        for (int i0 = 0; i0 < NV; i0 += kBatch)
-            fetch(raw_k, kbase, id0, i0, 0, kv_end);
-        cp_async_commit();
         for (int j = 0; j <= nk; ++j) {
             const int st = j % ST;
             const int id3 = id_of(j + 3);
