@@ -185,6 +185,14 @@ __device__ __noinline__ uint32_t note_nans(uint32_t w, int* nan_pos, int* any_na
     return w;
 }
 
+// Zero `rows` tokens' outputs of one KV head.
+__device__ __noinline__ void zero_rows(uint16_t* out, int64_t token_stride, int rows, int row_elems)
+{
+    for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5)
+        for (int i = (threadIdx.x & 31) * 2; i < row_elems; i += 64)
+            *reinterpret_cast<uint32_t*>(out + r * token_stride + i) = 0u;
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t a, const uint4& v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -253,10 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
         // zero rows; the last tile's CTA takes the rows no tile covers
         const int last = tile == ntiles - 1 ? n : min(n, j0 + span);
-        for (int64_t i = tid; i < (int64_t)(last - j0) * G * (D / 2); i += blockDim.x) {
-            const int64_t r = i / (D / 2);
-            reinterpret_cast<uint32_t*>(out + row_off(j0 + (int)(r / G), (int)(r % G)))[i % (D / 2)] = 0u;
-        }
+        zero_rows(out + row_off(j0, 0), (int64_t)p.num_heads * D, last - j0, G * D);
         return;
     }
     // the two query tiles: tokens [j0 + w QT, j0 + w QT + ntok_w)
@@ -575,12 +580,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld16(t_o + c0, *reinterpret_cast<uint32_t(*)[16]>(o32));
                     tmem_ld16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(o32 + 16));
                     tmem_wait_ld();
-                    if (nans) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (*reinterpret_cast<volatile int*>(&nan_pos[c0 + e]) <= pos)
-                                o32[e] = 0x7fffffffu;
-                    }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t o4[4];
@@ -591,6 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         st_shared16(qs + panel_off(r, c0 / 8 + c, kRows),
                                     make_uint4(o4[0], o4[1], o4[2], o4[3]));
                     }
+                }
+                if (nans) {
+                    // columns in which a key that the row sees has NaN
+#pragma unroll 1
+                    for (int d = 0; d < D; ++d)
+                        if (*reinterpret_cast<volatile int*>(&nan_pos[d]) <= pos)
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(qs + panel_off(r, d >> 3, kRows) +
+                                                                         (d & 7) * 2),
+                                         "h"((uint16_t)0x7fff)
+                                         : "memory");
                 }
                 __syncwarp();
                 const int c = lane % LPR;
