@@ -497,7 +497,7 @@ pkv_status pkv_paged_attention_decode_static_ws(const pkv_cache_desc* cache,
  *                s >= 2^-126 with bound <= 448 s.  A block whose first slot
  *                the call writes gets scale = need; any other block keeps the
  *                larger of its scale and need, and when that is larger than
- *                it was, the codes of its earlier tokens become
+ *                it was, the codes of its other slots become
  *                E4M3(code * old / new).  New codes are E4M3(x / scale), to
  *                nearest even; infinities saturate, NaN stays NaN.
  * q, k, v        device [total_q][num_heads or num_kv_heads][head_dim] of

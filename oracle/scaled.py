@@ -52,7 +52,8 @@ def append_scaled(codes, scales, which, new, raw, factor, cu, tables, ctx):
                     old = scales[phys, h, which]
                     sc = max(old, need)
                     if sc != old:
-                        o = codes[phys, h, :lo - b * bs]
+                        # every slot; those of the new tokens are written below
+                        o = codes[phys, h]
                         o[...] = encode_e4m3((dec(E4M3, o) * (float(old) / float(sc))).astype(np.float32))
                 scales[phys, h, which] = sc
                 # sc is a power of two: the fp32 quotient is the value's own rounding

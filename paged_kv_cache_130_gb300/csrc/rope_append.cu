@@ -335,10 +335,11 @@ __global__ void __launch_bounds__(kThreads, 4)
             const float sc = off > 0 ? fmaxf(old, need) : need;
             inv = 1.f / sc;
             if (off > 0 && sc != old) {
-                // the older tokens' codes follow the scale
+                // the codes of the block's other slots follow the scale
                 const float f = old / sc;
-                for (int i = lane; i < off * (D / 8); i += 32) {
-                    uint2* cp = reinterpret_cast<uint2*>(tile) + i;
+                for (int i = lane; i < (BS - T) * (D / 8); i += 32) {
+                    const int j = i < off * (D / 8) ? i : i + T * (D / 8);
+                    uint2* cp = reinterpret_cast<uint2*>(tile) + j;
                     const uint2 u = *cp;
                     float2 x[4];
                     const uint32_t ww[2] = {u.x, u.y};
