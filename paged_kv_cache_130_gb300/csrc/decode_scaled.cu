@@ -129,28 +129,46 @@ __device__ __forceinline__ int units_of(const DecodeParams& p, int s, bool flag)
 }
 
 // first[s] = units before sequence s (of one KV head), first[num_seqs] = all;
-// called by every thread of a CTA of at least 32 threads.
+// called by a whole CTA of kWarps warps.  Every thread takes a run of up to
+// kMaxBalanced / (32 kWarps) sequences, so that the lengths cost one round trip.
 __device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, bool flag)
 {
-    if (threadIdx.x < 32) {
-        int carry = 0;
-        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-            const int s = s0 + threadIdx.x;
-            int v = s < p.num_seqs ? units_of(p, s, flag) : 0;
-            const int own = v;
+    constexpr int kRun = kMaxBalanced / (32 * kWarps);
+    __shared__ int sums[kWarps];
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int per = ceil_div_i(p.num_seqs, 32 * kWarps);       // <= kRun
+    const int s0 = threadIdx.x * per;
+    int v[kRun];
+    int sum = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if ((int)threadIdx.x >= o)
-                    v += u;
-            }
-            if (s < p.num_seqs)
-                first[s] = carry + v - own;
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (threadIdx.x == 0)
-            first[p.num_seqs] = carry;
+    for (int i = 0; i < kRun; ++i)
+        v[i] = i < per && s0 + i < p.num_seqs ? units_of(p, s0 + i, flag) : 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+        sum += v[i];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += u;
     }
+    if (lane == 31)
+        sums[warp] = incl;
+    __syncthreads();
+    int at = incl - sum;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k)
+        at += k < warp ? sums[k] : 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        if (i < per && s0 + i < p.num_seqs)
+            first[s0 + i] = at;
+        at += v[i];
+    }
+    if (threadIdx.x == 32 * kWarps - 1)
+        first[p.num_seqs] = at;
     __syncthreads();
 }
 
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
 // Merge of the partials of the equal shares: one warp per (sequence, query
 // head).  Items that one CTA held whole are left alone; sequences without
 // tokens (or with an unusable length) get zeros.
-constexpr int kReduceRows = 4;
+constexpr int kReduceRows = kWarps;          // (scan_units wants kWarps warps)
 
 template <int QT, int D>
 __global__ void __launch_bounds__(kReduceRows * 32)

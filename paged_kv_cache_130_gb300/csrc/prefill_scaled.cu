@@ -458,8 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the factor of the scores stays positive: the scale's sign (or a
                 // scale of 0) goes into q
                 const float sign = p.qk_scale_log2 < 0.f ? -1.f : (p.qk_scale_log2 == 0.f ? 0.f : 1.f);
+                // (at least 1e-30, where the scores of such small keys vanish all
+                // the same: 0 times a masked key's -inf would be NaN)
                 qk = sign == 0.f ? 1.f
-                                 : fabsf(p.qk_scale_log2) * (1.f / up) * (kref * (1.f / kUnit));
+                                 : fmaxf(fabsf(p.qk_scale_log2) * (1.f / up) * (kref * (1.f / kUnit)), 1e-30f);
                 up *= sign;
                 if (up != 1.f || CT == kBF16)
 #pragma unroll 4

@@ -137,6 +137,12 @@ def check_rotated(got, x, ref, m, dt, what):
     assert not bad.any(), (what, int(bad.sum()), np.abs(got - ref).max())
 
 
+def canon(codes):
+    """Codes with one NaN: a re-rounded NaN stays one, of either sign."""
+    codes = codes.cpu().numpy() if isinstance(codes, torch.Tensor) else codes
+    return np.where(codes & 0x7f == 0x7f, 0x7f, codes)
+
+
 CASES = [
     # dtype, heads, kv, D, bs, new, cached, rot, interleaved, mscale
     (W.BF16, 4, 2, 128, 16, [1, 1, 1], [0, 16, 30], 128, False, 1.0),
@@ -162,10 +168,10 @@ def test_rope_append_scaled(i):
     check_rotated(q, b.q, rq, m if rot else 1.0, dt, "q")
     gs = b.gs.cpu().numpy()
     assert np.array_equal(gs, b.scales, equal_nan=True)
-    assert np.array_equal(b.gv.cpu().numpy(), b.v), "V codes"
+    assert np.array_equal(canon(b.gv), canon(b.v)), "V codes"
     gk = b.gk.cpu().numpy()
     if not rot:
-        assert np.array_equal(gk, b.k), "K codes"
+        assert np.array_equal(canon(gk), canon(b.k)), "K codes"
     else:
         # the new tokens' values; every other byte exactly
         same = np.ones(gk.shape, bool)
@@ -180,7 +186,7 @@ def test_rope_append_scaled(i):
                 bound = np.maximum(2.0 ** -4 * (np.abs(rk[row]) + e), 2.0 ** -10 * sc) + e
                 assert (np.abs(got - rk[row]) <= bound).all(), (s, p)
                 row += 1
-        assert np.array_equal(gk[same], b.k[same]), "bytes the call does not own"
+        assert np.array_equal(canon(gk[same]), canon(b.k[same])), "bytes the call does not own"
     assert int(b.err.item()) == 0
 
 
@@ -205,7 +211,7 @@ def test_rope_append_raises_the_scale_of_a_part_filled_block(bs):
             phys = b.tables[0, p // bs]
             assert (b.scales[phys] >= before[phys]).all()
     assert np.array_equal(b.gs.cpu().numpy(), b.scales, equal_nan=True)
-    assert np.array_equal(b.gk.cpu().numpy(), b.k) and np.array_equal(b.gv.cpu().numpy(), b.v)
+    assert np.array_equal(canon(b.gk), canon(b.k)) and np.array_equal(canon(b.gv), canon(b.v))
     assert int(b.err.item()) == 0
 
 
@@ -300,7 +306,7 @@ def test_rope_append_without_q_and_non_finite_inputs():
         got = oracle.decode(oracle.E4M3, x.gv.cpu().numpy())
         ref = oracle.decode(oracle.E4M3, b.v)
         assert np.array_equal(got, ref, equal_nan=True)
-        assert np.array_equal(x.gk.cpu().numpy(), b.k)
+        assert np.array_equal(canon(x.gk), canon(b.k))
     phys = b.tables[0, 0]
     assert oracle.decode(oracle.E4M3, b.v)[phys, 0, 1, 5] == 448
 
@@ -517,6 +523,37 @@ def test_attention_scaled_other_signs_of_the_scale(scale):
                              "decode scaled sign", W.F16)
 
 
+@pytest.mark.parametrize("zero", ["k", "v", "both"])
+def test_attention_scaled_over_zeros(zero):
+    """Contexts whose K, V or both are all zeros (the smallest scale there is):
+    the mean of V, or zeros."""
+    for new in ([70, 1], [1, 1]):
+        b = Batch(145, W.BF16, 4, 2, 64, 16, new, [40, 600])
+        for name in (("k",) if zero == "k" else ("v",) if zero == "v" else ("k", "v")):
+            getattr(b, name)[...] = 0
+            b.scales[..., "kv".index(name)] = 2.0 ** -126
+            getattr(b, "n" + name)[...] = 0
+        b.oracle_append()
+        b.upload()
+        out = b.prefill(0.125) if max(new) > 1 else b.decode(0.125)
+        H.assert_attention_close(H.out_to_double(out), b.attention(0.125), "zeros", W.BF16)
+
+
+@pytest.mark.parametrize("n", [1, 127, 128, 129, 1000, 1024, 1025])
+def test_decode_scaled_many_sequences(n):
+    """Batches around the number of sequences that equal shares scan (1,024)."""
+    r = np.random.default_rng(n)
+    ctx = r.integers(0, 40, n).astype(np.int32)
+    ctx[0] = 600                                   # long enough for equal shares
+    b = Batch(146, W.F16, 2, 1, 64, 16, [1] * n, ctx)
+    b.ctx, b.max_ctx = ctx, 600
+    b.gctx.copy_(torch.from_numpy(ctx))
+    assert (B.pkv_decode_scaled_partition_size(b.desc, n, 2, 600) == 0) == (n <= 1024)
+    out = b.decode(0.125)
+    H.assert_attention_close(H.out_to_double(out), b.attention(0.125), "many sequences", W.F16)
+    assert int(b.err.item()) == 0
+
+
 def test_prefill_scaled_nan_of_a_later_token_stays_there():
     """A NaN in K or V of a token reaches the rows that see the token (V: in its
     own column) and no other."""
@@ -597,3 +634,75 @@ def test_copy_blocks_scaled():
     B.pkv_copy_blocks_scaled(B.cache_desc(hk, hv), hs, back, descs[0], ss[0])
     for x in (ks[0], vs[0], ss[0]):
         assert torch.equal(x[9], x[7]) and torch.equal(x[10], x[8])
+
+
+def test_scaled_path_end_to_end():
+    """As an engine runs it: prompts appended and prefilled, every prompt forked
+    into three samples, copy-on-write with scales, twenty decode steps of append
+    and decode; each call against the oracle on the cache as it then is, and the
+    cache against the values that went in."""
+    from paged_kv_cache_130_gb300.block_manager import BlockManager, BlockPool
+    h, kv, d, bs, f = 8, 2, 64, 16, freqs(64)
+    r = np.random.default_rng(7)
+    mgr = BlockManager(BlockPool(200, bs, r.permutation(200)))
+    k8 = torch.full((200, kv, bs, d), 0xff, dtype=torch.uint8, device="cuda")
+    v8, sc = k8.clone(), torch.full((200, kv, 2), float("nan"), device="cuda")
+    desc = B.cache_desc(k8, v8)
+    gf = torch.from_numpy(f).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = {}                                      # sequence -> its (K rotated, V) rows so far
+
+    def call(seqs, new):
+        """Append `new` tokens to each sequence and attend; returns nothing."""
+        n = sum(new)
+        x = [torch.from_numpy(r.standard_normal((n, m, d))).bfloat16().cuda() for m in (h, kv, kv)]
+        ctx = np.array([s.num_tokens for s in seqs], np.int32)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        bt = BlockManager.block_table_array(seqs)
+        g = [torch.from_numpy(a).cuda() for a in (cu, bt, ctx)]
+        q = B.pkv_rope_append(desc, *x, gf, g[0], max(new), g[1], g[2], int(ctx.max()), scales=sc,
+                              dev_err=err)
+        if max(new) > 1:
+            out = B.pkv_paged_attention_prefill_scaled(desc, sc, q, g[0], max(new), g[1], g[2],
+                                                       int(ctx.max()), 0.125, dev_err=err)
+        else:
+            out = B.pkv_paged_attention_decode_scaled(desc, sc, q, g[1], g[2], int(ctx.max()), 0.125,
+                                                      dev_err=err)
+        kc, vc, s_ = k8.cpu().numpy(), v8.cpu().numpy(), sc.cpu().numpy()
+        ref = OS.attention(kc, vc, s_, q.double().cpu().numpy(), cu, bt, ctx, 0.125)
+        H.assert_attention_close(H.out_to_double(out), ref, "path", W.BF16)
+        pos = np.concatenate([np.arange(c - m, c) for c, m in zip(ctx, new)])
+        rk = OS.rotate(x[1].double().cpu().numpy(), pos, f)
+        for i, s in enumerate(seqs):
+            rows = slice(cu[i], cu[i + 1])
+            old = kept.get(id(s), (np.zeros((0, kv, d)),) * 2)
+            kept[id(s)] = tuple(np.concatenate([a, b[rows]]) for a, b in
+                                zip(old, (rk, x[2].double().cpu().numpy())))
+            for which, codes in ((0, kc), (1, vc)):
+                for hd in range(kv):
+                    got = OS.gather(codes, s_, which, bt[i], int(ctx[i]), hd)
+                    want = kept[id(s)][which][:, hd]
+                    # E4M3 of the value, and a second rounding where a later token
+                    # raised the block's scale: half a step of the value, and half
+                    # a subnormal step of each scale that its block has had
+                    top = s_[bt[i, :-(-int(ctx[i]) // bs)], hd, which].repeat(bs)[:int(ctx[i]), None]
+                    bound = 2.0 ** -4 * 1.0625 * np.abs(want) + 2.0 ** -9 * top + 1e-5
+                    assert (np.abs(got - want) <= bound).all()
+
+    prompts = [mgr.new_sequence() for _ in range(3)]
+    lens = [37, 130, 16]
+    for s, n in zip(prompts, lens):
+        mgr.append_tokens(s, n)
+    call(prompts, lens)
+    seqs = []
+    for s in prompts:
+        for t in [s] + [mgr.fork(s) for _ in range(2)]:
+            kept[id(t)] = kept[id(s)]
+            seqs.append(t)
+    for step in range(20):
+        pairs = [p for _, p in (mgr.append_slot(s) for s in seqs) if p is not None]
+        if pairs:
+            assert step == 0
+            B.pkv_copy_blocks_scaled(desc, sc, torch.tensor(pairs, device="cuda"), dev_err=err)
+        call(seqs, [1] * len(seqs))
+    assert int(err.item()) == 0
