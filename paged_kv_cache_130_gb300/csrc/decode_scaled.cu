@@ -42,7 +42,6 @@ using dec::PartitionWork;
 
 constexpr int kWarps = 4;
 constexpr int kMaxGroup = 16;          // query heads per KV head
-constexpr int kOnePass = 512;          // tokens: contexts up to here are one CTA's work
 constexpr float kRaise = 8.f;          // log2: how far a score may pass the maximum
 constexpr float kWeightScale = 64.f;
 
@@ -211,39 +210,52 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     pdl_wait_primary();
     pdl_launch_dependents();
 
-    int64_t at = 0, end = 1;                   // BAL: the CTA's units
+    // BAL: units left of the CTA's share, and where it stands: unit u0 of KV
+    // head bal_h of sequence bal_s
+    int64_t left = 1;
+    int bal_s = 0, bal_h = 0, u0 = 0;
     if constexpr (BAL) {
         scan_units(p, sm_first, blockIdx.x == 0);
         const Shares sh = shares_of(p, sm_first, gridDim.x);
         if ((int64_t)blockIdx.x >= sh.ctas)
             return;
-        at = sh.begin(blockIdx.x);
-        end = sh.begin(blockIdx.x + 1);
+        const int64_t at = sh.begin(blockIdx.x);
+        left = sh.begin(blockIdx.x + 1) - at;
+        int hi = p.num_seqs;                   // the last s with first[s] Hkv <= at
+        while (hi - bal_s > 1) {
+            const int mid = (bal_s + hi) >> 1;
+            if ((int64_t)sm_first[mid] * p.num_kv_heads <= at)
+                bal_s = mid;
+            else
+                hi = mid;
+        }
+        const int n = sm_first[bal_s + 1] - sm_first[bal_s];
+        const int64_t in = at - (int64_t)sm_first[bal_s] * p.num_kv_heads;
+        bal_h = (int)(in / n);
+        u0 = (int)(in - (int64_t)bal_h * n);
     }
-    while (at < end) {
+    while (left > 0) {
     int s, head, t_begin, t_end;
     bool direct;
     int64_t prow;                              // first row of the partial
     if constexpr (BAL) {
-        int lo = 0, hi = p.num_seqs;           // the last s with first[s] Hkv <= at
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((int64_t)sm_first[mid] * p.num_kv_heads <= at)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        s = lo;
+        s = bal_s;
+        head = bal_h;
         const int n = sm_first[s + 1] - sm_first[s];
-        const int64_t in = at - (int64_t)sm_first[s] * p.num_kv_heads;
-        head = (int)(in / n);
-        const int u0 = (int)(in - (int64_t)head * n);
-        const int u1 = (int)min((int64_t)n, u0 + (end - at));
+        const int u1 = (int)min((int64_t)n, u0 + left);
         t_begin = u0 * kUnit;
         t_end = min(__ldg(p.context_lens + s), u1 * kUnit);
         direct = u0 == 0 && u1 == n;
         prow = (2 * (int64_t)blockIdx.x + (u0 == 0 ? 1 : 0)) * RT;
-        at += u1 - u0;
+        left -= u1 - u0;
+        // the next item: the next head, or head 0 of the next sequence with tokens
+        u0 = 0;
+        if (++bal_h == p.num_kv_heads && left > 0) {
+            bal_h = 0;
+            do
+                ++bal_s;
+            while (sm_first[bal_s + 1] == sm_first[bal_s]);
+        }
     } else {
         int64_t idx = blockIdx.x;
         head = (int)(idx % p.num_kv_heads);
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         t_end = w.t_end;
         direct = w.direct;
         prow = dec::partial_row(p, s, head * G, w.slot);
-        at = end;
+        left = 0;
     }
 
     // q: each warp scales rows warp, warp + 4, ... by a power of two that
@@ -568,8 +580,8 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
             *reinterpret_cast<float2*>(p.ws_o + row * D + d) = make_float2(o0, o1);
         }
     }
-    if (BAL)
-        __syncthreads();                       // the next item reuses the tables
+    // (the next item's q is filed once every warp is past the barrier above, its
+    // states once every warp is past the one behind q)
     }
 }
 
@@ -601,6 +613,7 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         acc[e] = 0.f;
     float L = 0.f;
     pdl_wait_primary();
+    pdl_launch_dependents();
     if (n > 0) {
         const int64_t x = (int64_t)sm_first[s] * p.num_kv_heads + (int64_t)head * n;
         const int64_t c0 = sh.owner(x);
@@ -723,10 +736,17 @@ int64_t decode_scaled_partial_rows(int32_t group, int sms)
 
 // One CTA per (sequence, KV head), in one launch, while the longest context is
 // short; equal shares beyond, unless there are more sequences than a CTA scans.
-int32_t decode_scaled_partition(const DecodeParams& p)
+// Measured, D = 128, one pass / shares in us: 32 items of 128..512 tokens 7.3 /
+// 10.3, 512 of 512..2048 47 / 43, 2,048 of 256..1024 70 / 73, of 512..2048 124 /
+// 123, of 1024..4096 231 / 220, 8,192 of 1024..4096 837 / 863, of 2048..8192
+// 1633 / 1651: the shares' second launch and their walk cost some 3 us and 1 us
+// an item, one pass the imbalance of its last wave.
+int32_t decode_scaled_partition(const DecodeParams& p, int sms)
 {
     const int32_t bs = p.block_size < 16 ? 16 : p.block_size;
-    if (p.max_context_len <= kOnePass)
+    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads;
+    const int32_t group = p.num_heads / p.num_kv_heads;
+    if (p.max_context_len <= 1024 + 256 * items / decode_scaled_ctas(group, sms))
         return (p.max_context_len + bs - 1) / bs * bs;
     return p.num_seqs <= kMaxBalanced ? 0 : (1 << 19) / (2 * p.head_dim);
 }

@@ -544,11 +544,11 @@ def test_decode_scaled_many_sequences(n):
     """Batches around the number of sequences that equal shares scan (1,024)."""
     r = np.random.default_rng(n)
     ctx = r.integers(0, 40, n).astype(np.int32)
-    ctx[0] = 600                                   # long enough for equal shares
+    ctx[0] = 2000                                  # long enough for equal shares
     b = Batch(146, W.F16, 2, 1, 64, 16, [1] * n, ctx)
-    b.ctx, b.max_ctx = ctx, 600
+    b.ctx, b.max_ctx = ctx, 2000
     b.gctx.copy_(torch.from_numpy(ctx))
-    assert (B.pkv_decode_scaled_partition_size(b.desc, n, 2, 600) == 0) == (n <= 1024)
+    assert (B.pkv_decode_scaled_partition_size(b.desc, n, 2, 2000) == 0) == (n <= 1024)
     out = b.decode(0.125)
     H.assert_attention_close(H.out_to_double(out), b.attention(0.125), "many sequences", W.F16)
     assert int(b.err.item()) == 0
