@@ -130,10 +130,10 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* fl
     return ok;
 }
 
-// A power of two at or above every scale up to x (positive, finite; 1 for 0).
-__device__ __forceinline__ float reference_of(float x)
+// A power of two at or above every scale up to the one whose bits these are.
+__device__ __forceinline__ float reference_of(const uint32_t* bits)
 {
-    const uint32_t e = __float_as_uint(x) & 0x7f800000u;
+    const uint32_t e = *reinterpret_cast<const volatile uint32_t*>(bits) & 0x7f800000u;
     if (e == 0)
         return 1.1754944e-38f;
     return e >= 0x7e800000u ? 1.7014118e38f : __uint_as_float(e + 0x00800000u);
@@ -278,6 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t raw = s_addr(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
+    // the scan of the scales below: its first ids (of up to 512 blocks) are asked
+    // for here, the scales when the ids have come
+    const int nblocks = (kv_end + BS - 1) / BS;
+    const int id_first = tid < nblocks ? __ldg(table + tid) : 0;
 
     if (tid == 0) {
 #pragma unroll
@@ -310,7 +314,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                      "r"(L::cols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder;
+    auto block_ok = [&](int phys) { return phys >= 0 && (int64_t)phys < p.num_blocks; };
+    float2 sc_first = make_float2(0.f, 0.f);
+    if (tid < nblocks) {
+        if (block_ok(id_first))
+            sc_first = __ldg(scales + (int64_t)id_first * p.num_kv_heads + g);
+        else
+            flag_error(p.dev_err, PKV_DEVERR_BLOCK_ID);
+    }
     // ---------------- what can start before the scales are known ----------------
     // Softmax warps: q, in its own type.  A warp copies its 32 rows side by side
     // into their places; rows past the tile's are zero.
@@ -361,7 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = kt * kKeys + lane * BS;
         return kt < nk && lane < NB && tok < kv_end ? __ldg(table + tok / BS) : -1;
     };
-    auto good = [&](int phys) { return phys >= 0 && (int64_t)phys < p.num_blocks; };
     // Codes travel through a staging area in which every thread has places of
     // its own (vector i at i * 128 + thread): copied asynchronously one slot
     // ahead, read back and converted by the thread that asked for them, so
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < kBatch; u += NP) {
             const int row = (i0 + u) / NP * 32 + rsub;
             const int phys = __shfl_sync(0xffffffffu, id, row / BS);
-            const bool ok = good(phys) && first + row < end;
+            const bool ok = block_ok(phys) && first + row < end;
             const unsigned char* src = base + (ok ? phys * stride + (row % BS) * D + c4 * 16 : 0);
 #pragma unroll
             for (int q = 0; q < NP; ++q)
@@ -392,17 +406,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             fetch(raw_k, kbase, id0, i0, 0, kv_end);
         cp_async_commit();
     }
-    // the largest scales of the CTA's blocks
+    // the largest scales of the CTA's blocks (positive floats order as their
+    // bits; anything else counts as 0)
     {
-        uint32_t mk = 0, mv = 0;
-        for (int b = tid; b * BS < kv_end; b += kThreads) {
+        uint32_t mk = sc_first.x > 0.f ? __float_as_uint(sc_first.x) : 0u;
+        uint32_t mv = sc_first.y > 0.f ? __float_as_uint(sc_first.y) : 0u;
+        for (int b = tid + kThreads; b < nblocks; b += kThreads) {
             const int phys = __ldg(table + b);
-            if (phys < 0 || (int64_t)phys >= p.num_blocks) {
+            if (!block_ok(phys)) {
                 flag_error(p.dev_err, PKV_DEVERR_BLOCK_ID);
                 continue;
             }
             const float2 sc = __ldg(scales + (int64_t)phys * p.num_kv_heads + g);
-            // positive floats order as their bits; anything else counts as 0
             if (sc.x > 0.f)
                 mk = max(mk, __float_as_uint(sc.x));
             if (sc.y > 0.f)
@@ -415,12 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicMax(&ref_bits[1], mv);
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_holder;
-    const float kref = reference_of(__uint_as_float(ref_bits[0]));
-    const float vref = reference_of(__uint_as_float(ref_bits[1]));
+    // The converting warps wait for everybody's part; the others read the maxima
+    // when the first slot, which those warps fill, has come to them.
+    if (warp >= kConvWarp)
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    else
+        asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
 
     if (warp < 8) {
         // ---------------- softmax of query tile w ----------------
@@ -458,10 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the factor of the scores stays positive: the scale's sign (or a
                 // scale of 0) goes into q
                 const float sign = p.qk_scale_log2 < 0.f ? -1.f : (p.qk_scale_log2 == 0.f ? 0.f : 1.f);
-                // (at least 1e-30, where the scores of such small keys vanish all
-                // the same: 0 times a masked key's -inf would be NaN)
-                qk = sign == 0.f ? 1.f
-                                 : fmaxf(fabsf(p.qk_scale_log2) * (1.f / up) * (kref * (1.f / kUnit)), 1e-30f);
+                qk = sign == 0.f ? 0.f : fabsf(p.qk_scale_log2) * (1.f / up) * (1.f / kUnit);
                 up *= sign;
                 if (up != 1.f || CT == kBF16)
 #pragma unroll 4
@@ -493,6 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                // K's reference, with the first keys.  (At least 1e-30, where the
+                // scores of such small keys vanish all the same: 0 times a masked
+                // key's -inf would be NaN.)
+                if (kt == 0)
+                    qk = fmaxf(qk * reference_of(&ref_bits[0]), 1e-30f);
                 float x[kKeys];
 #pragma unroll
                 for (int c0 = 0; c0 < kKeys; c0 += 16)
@@ -500,9 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld();
                 // causal mask only where some key passes some row's position
                 if (kt * kKeys + kKeys - 1 > pos0) {
+                    const int lim = pos - kt * kKeys;      // the last key the row sees
 #pragma unroll
-                    for (int j = 0; j < kKeys; ++j)
-                        x[j] = kt * kKeys + j <= pos ? x[j] : kNegInf;
+                    for (int j0 = 0; j0 < kKeys; j0 += 32) {
+                        const int n = lim - j0 + 1;
+                        const uint32_t bits = n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[j0 + j] = (bits >> j) & 1u ? x[j0 + j] : kNegInf;
+                    }
                 }
                 // row max: eight independent chains of three-input maxima
                 float mc[8];
@@ -571,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alive) {
                 // epilogue: O / l for this thread's row
                 tc_fence_after();
-                const float inv = l_run > 0.f ? (1.f / l_run) * (vref * (1.f / kUnit))
+                const float inv = l_run > 0.f ? (1.f / l_run) * (reference_of(&ref_bits[1]) * (1.f / kUnit))
                                               : (l_run == 0.f ? 0.f : l_run);
                 const bool nans = *reinterpret_cast<volatile int*>(&any_nan) != 0;
                 // through shared memory (this tile's q, which every product has
@@ -697,10 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         // ---------------- load and convert (four warps) ----------------
         auto scales_of = [&](int phys) -> float2 {
-            return good(phys) ? __ldg(scales + (int64_t)phys * p.num_kv_heads + g) : make_float2(0.f, 0.f);
+            return block_ok(phys) ? __ldg(scales + (int64_t)phys * p.num_kv_heads + g) : make_float2(0.f, 0.f);
         };
         // (the references are powers of two: their inverses are exact)
-        const float kinv = 1.f / kref, vinv = 1.f / vref;
+        const float kinv = 1.f / reference_of(&ref_bits[0]), vinv = 1.f / reference_of(&ref_bits[1]);
         auto factor = [&](float sc, float inv) -> uint32_t {
             const float f = sc * inv * kUnit;
             return pack_rn<kF16>(f, f);
