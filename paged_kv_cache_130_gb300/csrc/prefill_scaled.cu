@@ -432,10 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // The converting warps wait for everybody's part; the others read the maxima
     // when the first slot, which those warps fill, has come to them.
-    if (warp >= kConvWarp)
+    // (They give their registers up before that: the softmax warps' q waits for
+    // the registers.)
+    if (warp >= kConvWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-    else
+    } else {
         asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+    }
 
     if (warp < 8) {
         // ---------------- softmax of query tile w ----------------
@@ -717,7 +721,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_wait(s_addr(&bars.drain[w]), 0);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         // ---------------- load and convert (four warps) ----------------
         auto scales_of = [&](int phys) -> float2 {
             return block_ok(phys) ? __ldg(scales + (int64_t)phys * p.num_kv_heads + g) : make_float2(0.f, 0.f);
