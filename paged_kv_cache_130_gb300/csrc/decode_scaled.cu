@@ -98,21 +98,39 @@ __device__ __forceinline__ uint2 ld_stream8(const void* p)
 }
 
 // Equal shares: tokens of every (sequence, KV head) in units of kUnit, laid end
-// to end (sequence, then head, then position); CTA c of C takes units
-// [c T / C, (c + 1) T / C) of the T there are, whatever items they belong to.
-// An item that one CTA holds whole is written out; a CTA has at most two
-// others, which it files as partials 2 c + 1 (starts at the item's first token)
-// and 2 c (starts inside the item), and the reduce kernel finds an item's
-// partials from the same arithmetic.
+// to end (sequence, then head, then position), kItemUnits units without tokens in
+// front of each item for what starting it costs; CTA c of C takes units
+// [floor(c T / C), floor((c + 1) T / C)) of the T there are, whatever items they
+// belong to.  An item whose tokens one CTA holds whole is written out; a CTA has
+// at most two others, which it files as partials 2 c + 1 (starts at the item's
+// first token) and 2 c (starts inside the item), and the reduce kernel finds an
+// item's partials from the same arithmetic.
 constexpr int kUnit = 16 * kWarps;         // tokens: one step for each warp
-constexpr int kMinUnits = 4;               // smallest share
+constexpr int kItemUnits = 3;              // merge, q and first codes: ~4 us beside ~1.1 us a unit
+constexpr int kMinUnits = 8;               // smallest share
+// (a share has at least kMinUnits / 2 units: 9 in two are 4 and 5)
+static_assert(kMinUnits / 2 > kItemUnits, "at most one CTA of an item has none of its tokens");
 constexpr int kMaxBalanced = 1024;         // sequences
 
 struct Shares {
     int64_t total;                         // units
-    int64_t ctas;                          // CTAs that have any
-    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * total / ctas; }
-    __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * ctas - 1) / total; }
+    uint32_t ctas;                         // CTAs that have any
+    int64_t each;                          // total / ctas
+    uint32_t rest;                         // total % ctas
+    __device__ __forceinline__ int64_t begin(uint32_t c) const
+    {
+        return c * each + c * rest / ctas;       // (ctas < 2^16: 32 bits hold c rest)
+    }
+    // the CTA that holds unit x
+    __device__ __forceinline__ uint32_t owner(int64_t x) const
+    {
+        uint32_t c = min(ctas - 1, (uint32_t)((float)x * (float)ctas / (float)total));
+        while (c > 0 && begin(c) > x)
+            --c;
+        while (c + 1 < ctas && begin(c + 1) <= x)
+            ++c;
+        return c;
+    }
 };
 
 // Units of sequence s: 0 for an empty context and for one that cannot be used.
@@ -124,7 +142,7 @@ __device__ __forceinline__ int units_of(const DecodeParams& p, int s, bool flag)
             flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
         return 0;
     }
-    return ceil_div_i(ctx, kUnit);
+    return ctx > 0 ? ceil_div_i(ctx, kUnit) + kItemUnits : 0;
 }
 
 // first[s] = units before sequence s (of one KV head), first[num_seqs] = all;
@@ -171,12 +189,20 @@ __device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, bo
     __syncthreads();
 }
 
-__device__ __forceinline__ Shares shares_of(const DecodeParams& p, const int* first, int64_t ctas)
+__device__ __forceinline__ Shares shares_of(const DecodeParams& p, const int* first, uint32_t ctas)
 {
     Shares sh;
     sh.total = (int64_t)first[p.num_seqs] * p.num_kv_heads;
-    const int64_t most = (sh.total + kMinUnits - 1) / kMinUnits;
-    sh.ctas = most < ctas ? most : ctas;
+    sh.ctas = min((int64_t)ctas, (sh.total + kMinUnits - 1) / kMinUnits);
+    if (sh.ctas == 0) {
+        sh.each = sh.rest = 0;
+    } else if (sh.total <= 0xffffffffll) {
+        sh.each = (uint32_t)sh.total / sh.ctas;          // (64-bit divisions are long)
+        sh.rest = (uint32_t)sh.total % sh.ctas;
+    } else {
+        sh.each = sh.total / sh.ctas;
+        sh.rest = (uint32_t)(sh.total % sh.ctas);
+    }
     return sh;
 }
 
@@ -217,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     if constexpr (BAL) {
         scan_units(p, sm_first, blockIdx.x == 0);
         const Shares sh = shares_of(p, sm_first, gridDim.x);
-        if ((int64_t)blockIdx.x >= sh.ctas)
+        if (blockIdx.x >= sh.ctas)
             return;
         const int64_t at = sh.begin(blockIdx.x);
         left = sh.begin(blockIdx.x + 1) - at;
@@ -231,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         }
         const int n = sm_first[bal_s + 1] - sm_first[bal_s];
         const int64_t in = at - (int64_t)sm_first[bal_s] * p.num_kv_heads;
-        bal_h = (int)(in / n);
+        bal_h = in <= 0xffffffffll ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
         u0 = (int)(in - (int64_t)bal_h * n);
     }
     while (left > 0) {
@@ -243,10 +269,10 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         head = bal_h;
         const int n = sm_first[s + 1] - sm_first[s];
         const int u1 = (int)min((int64_t)n, u0 + left);
-        t_begin = u0 * kUnit;
-        t_end = min(__ldg(p.context_lens + s), u1 * kUnit);
-        direct = u0 == 0 && u1 == n;
-        prow = (2 * (int64_t)blockIdx.x + (u0 == 0 ? 1 : 0)) * RT;
+        t_begin = max(u0 - kItemUnits, 0) * kUnit;
+        t_end = min(__ldg(p.context_lens + s), (u1 - kItemUnits) * kUnit);
+        direct = u0 <= kItemUnits && u1 == n;
+        prow = (2 * (int64_t)blockIdx.x + (u0 <= kItemUnits ? 1 : 0)) * RT;
         left -= u1 - u0;
         // the next item: the next head, or head 0 of the next sequence with tokens
         u0 = 0;
@@ -256,6 +282,8 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
                 ++bal_s;
             while (sm_first[bal_s + 1] == sm_first[bal_s]);
         }
+        if (u1 <= kItemUnits)
+            break;                             // the share ends before the item's tokens
     } else {
         int64_t idx = blockIdx.x;
         head = (int)(idx % p.num_kv_heads);
@@ -616,19 +644,21 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     pdl_launch_dependents();
     if (n > 0) {
         const int64_t x = (int64_t)sm_first[s] * p.num_kv_heads + (int64_t)head * n;
-        const int64_t c0 = sh.owner(x);
-        const int64_t c1 = sh.owner(x + n - 1);
+        uint32_t c0 = sh.owner(x);
+        const uint32_t c1 = sh.owner(x + n - 1);
+        if (c0 < c1 && sh.begin(c0 + 1) - x <= kItemUnits)
+            ++c0;                              // (its share ended before the item's tokens)
         if (c0 == c1)
             return;
         float M = kNegInf;
-        for (int64_t c = c0 + lane; c <= c1; c += 32)
-            M = fmaxf(M, p.ws_m[(2 * c + (c == c0 ? 1 : 0)) * rows_per_partial + r]);
+        for (uint32_t c = c0 + lane; c <= c1; c += 32)
+            M = fmaxf(M, p.ws_m[(2 * (int64_t)c + (c == c0 ? 1 : 0)) * rows_per_partial + r]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll 4
-        for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t pr = (2 * c + (c == c0 ? 1 : 0)) * rows_per_partial + r;
+        for (uint32_t c = c0; c <= c1; ++c) {
+            const int64_t pr = (2 * (int64_t)c + (c == c0 ? 1 : 0)) * rows_per_partial + r;
             const float m = p.ws_m[pr];
             const float f = m == kNegInf ? 0.f : exp2_fast(m - M);
             L += f * p.ws_l[pr];
