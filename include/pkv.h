@@ -533,18 +533,17 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
  * Decode attention over a scaled cache: pkv_paged_attention_decode with k_t and
  * v_t = code * scale of their block and KV head.  q and out F16 or BF16, 1..16
  * query heads per KV head; partition_size a multiple of block_size and of 16,
- * or 0 for the library's choice: one CTA per sequence and KV head (one launch, no
- * workspace) while max_context_len is at most 1024 + 256 x (num_seqs *
- * num_kv_heads / the CTAs that fit the GPU at once: three per SM, two above
- * eight query heads per KV head); beyond that equal shares of the batch's tokens
- * for those CTAs, merged by a second launch.  An explicit
+ * or 0 for the library's choice: contexts up to 1,024 tokens one CTA per sequence
+ * and KV head (one launch, no workspace), beyond that equal shares of the batch's
+ * tokens for the CTAs that fit the GPU at once (three per SM, two above eight
+ * query heads per KV head), merged by a second launch.  An explicit
  * partition_size gives the partitions, workspace layout and reduce of
  * pkv_paged_attention_decode.  pkv_decode_scaled_partition_size tells the choice
  * (0: equal shares), pkv_decode_scaled_workspace_bytes the scratch it needs.
  * A block with a bad id contributes nothing.  The same inputs and partition
  * size give the same bits on one kind of GPU.
- * Scales are positive and finite; V's small next to the largest of the context
- * lose no precision down to a ratio of 2^-20.
+ * Scales are positive and finite; V of a block loses no precision while its scale
+ * is within 2^20 of the context's largest.
  * ------------------------------------------------------------------------- */
 int32_t pkv_decode_scaled_partition_size(const pkv_cache_desc* cache, int32_t num_seqs,
                                          int32_t num_heads, int32_t max_context_len,

@@ -42,6 +42,7 @@ using dec::PartitionWork;
 
 constexpr int kWarps = 4;
 constexpr int kMaxGroup = 16;          // query heads per KV head
+constexpr int kOnePass = 1024;         // tokens: contexts up to here are one CTA's work
 constexpr float kRaise = 8.f;          // log2: how far a score may pass the maximum
 constexpr float kWeightScale = 64.f;
 
@@ -767,16 +768,14 @@ int64_t decode_scaled_partial_rows(int32_t group, int sms)
 // One CTA per (sequence, KV head), in one launch, while the longest context is
 // short; equal shares beyond, unless there are more sequences than a CTA scans.
 // Measured, D = 128, one pass / shares in us: 32 items of 128..512 tokens 7.3 /
-// 10.3, 512 of 512..2048 47 / 43, 2,048 of 256..1024 70 / 73, of 512..2048 124 /
-// 123, of 1024..4096 231 / 220, 8,192 of 1024..4096 837 / 863, of 2048..8192
-// 1633 / 1651: the shares' second launch and their walk cost some 3 us and 1 us
-// an item, one pass the imbalance of its last wave.
-int32_t decode_scaled_partition(const DecodeParams& p, int sms)
+// 11.5, 128 (8 heads each) of 128..512 8.6 / 15.5, 1,024 of 256..1024 44 / 44, of
+// 512..2048 76 / 71, of 1024..4096 137 / 120, 2,048 of 256..1024 70 / 69, of
+// 1024..4096 232 / 216, 8,192 of 256..1024 249 / 248, of 2048..8192 1633 / 1634:
+// the shares' second launch and walk against the imbalance of the last wave.
+int32_t decode_scaled_partition(const DecodeParams& p)
 {
     const int32_t bs = p.block_size < 16 ? 16 : p.block_size;
-    const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads;
-    const int32_t group = p.num_heads / p.num_kv_heads;
-    if (p.max_context_len <= 1024 + 256 * items / decode_scaled_ctas(group, sms))
+    if (p.max_context_len <= kOnePass)
         return (p.max_context_len + bs - 1) / bs * bs;
     return p.num_seqs <= kMaxBalanced ? 0 : (1 << 19) / (2 * p.head_dim);
 }

@@ -110,7 +110,7 @@ int32_t partition_of(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_head
     p.num_seqs = num_seqs;
     p.num_heads = num_heads;
     p.max_context_len = max_context_len;
-    return pkv::decode_scaled_partition(p, device_sms());
+    return pkv::decode_scaled_partition(p);
 }
 
 bool sizes_known(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads,

@@ -53,7 +53,7 @@ cudaError_t launch_decode_scaled(const DecodeParams& p, const float* scales, int
 int64_t decode_scaled_ctas(int32_t group, int sms);
 int64_t decode_scaled_partial_rows(int32_t group, int sms);
 // The library's choice: tokens per partition, or 0 for equal shares.
-int32_t decode_scaled_partition(const DecodeParams& p, int sms);
+int32_t decode_scaled_partition(const DecodeParams& p);
 
 struct ScaledPrefillParams {
     PrefillParams p;               // dtype = that of q and out

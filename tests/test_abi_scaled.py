@@ -127,14 +127,13 @@ def test_workspace_follows_the_partition(lib):
     assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 1000, 1008) == 0
     ml = -(-4 * 4 * 64 * 16 // 256) * 256
     assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 1000, 64) == 2 * ml + 4 * 4 * 64 * 16 * 128
-    # the library's choice: one partition, without a workspace, while contexts
-    # are short for the number of items; equal shares beyond, with a workspace
-    # that the batch does not change (456 CTAs: 152 SMs without a GPU)
+    # the library's choice: one partition, without a workspace, for contexts up
+    # to 1,024 tokens; equal shares beyond, with a workspace that the batch does
+    # not change
     assert B.pkv_decode_scaled_partition_size(d, 4, 64, 500) == 512
     assert B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 500) == 0
-    assert B.pkv_decode_scaled_partition_size(d, 4, 64, 1041) == 1056       # 1024 + 256 x 32 / 456
-    assert B.pkv_decode_scaled_partition_size(d, 4, 64, 1042) == 0
-    assert B.pkv_decode_scaled_partition_size(d, 900, 64, 5000) == 5008
+    assert B.pkv_decode_scaled_partition_size(d, 900, 64, 1024) == 1024
+    assert B.pkv_decode_scaled_partition_size(d, 4, 64, 1025) == 0
     n = B.pkv_decode_scaled_workspace_bytes(d, 4, 64, 2000)
     assert n > 0 and n == B.pkv_decode_scaled_workspace_bytes(d, 900, 64, 100000)
     p = B.pkv_decode_scaled_partition_size(d, 2000, 64, 100000)

@@ -706,3 +706,85 @@ def test_scaled_path_end_to_end():
             B.pkv_copy_blocks_scaled(desc, sc, torch.tensor(pairs, device="cuda"), dev_err=err)
         call(seqs, [1] * len(seqs))
     assert int(err.item()) == 0
+
+
+def test_scaled_calls_beyond_four_gigabytes():
+    """Blocks whose byte offsets pass 32 bits: the same bits as the same blocks
+    at the front of a pool."""
+    b = Batch(150, W.BF16, 8, 2, 128, 32, [70, 1, 40], [100, 1200, 0])
+    f = torch.from_numpy(freqs(128)).cuda()
+    n = (1 << 32) // (2 * 32 * 128) + 1000          # K codes alone past 2^32 bytes
+    far = [torch.empty(n, 2, 32, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    fs = torch.empty(n, 2, 2, device="cuda")
+    at = n - b.nb
+    for t, src in zip(far + [fs], (b.gk, b.gv, b.gs)):
+        t[at:] = src
+    desc, tables = B.cache_desc(*far), torch.where(b.gt >= 0, b.gt + at, b.gt)
+    args = [b.dev16(x) for x in (b.q, b.nk, b.nv)]
+    outs = []
+    for d, s, t in ((b.desc, b.gs, b.gt), (desc, fs, tables)):
+        q = B.pkv_rope_append(d, *args, f, b.gcu, b.max_new, t, b.gctx, b.max_ctx, scales=s,
+                              dev_err=b.err)
+        pre = B.pkv_paged_attention_prefill_scaled(d, s, q, b.gcu, b.max_new, t, b.gctx, b.max_ctx,
+                                                   0.1, dev_err=b.err)
+        dec = B.pkv_paged_attention_decode_scaled(d, s, q[b.gcu[1:].long() - 1].contiguous(), t,
+                                                  b.gctx, b.max_ctx, 0.1, dev_err=b.err)
+        outs.append((q, pre, dec))
+    B.pkv_copy_blocks_scaled(desc, fs, torch.tensor([[at + 1, 0], [at + 2, at + 3]], device="cuda"),
+                             dev_err=b.err)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == 0
+    for x, y in zip(*outs):
+        assert torch.equal(x, y) and not x.isnan().any()
+    for t in far + [fs]:
+        for src, dst in ((at + 1, 0), (at + 2, at + 3)):
+            assert torch.equal(t[dst].view(torch.uint8), t[src].view(torch.uint8))
+    keep = [i for i in range(b.nb) if i != 3]
+    assert torch.equal(far[0][at:][keep], b.gk[keep]) and torch.equal(far[1][at:][keep], b.gv[keep])
+
+
+def test_scaled_calls_with_nothing_to_do():
+    b = Batch(151, W.F16, 4, 2, 64, 16, [1], [20])
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    rows = [torch.empty(0, h, 64, dtype=torch.float16, device="cuda") for h in (4, 2, 2)]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    empty_table = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    q = B.pkv_rope_append(b.desc, *rows, None, zero, 0, empty_table, none, 0, scales=b.gs)
+    assert q.shape == (0, 4, 64)
+    out = B.pkv_paged_attention_decode_scaled(b.desc, b.gs, rows[0], empty_table, none, 0, 0.1)
+    assert out.shape == (0, 4, 64)
+    out = B.pkv_paged_attention_prefill_scaled(b.desc, b.gs, rows[0], zero, 0, empty_table, none, 0, 0.1)
+    assert out.shape == (0, 4, 64)
+    B.pkv_copy_blocks_scaled(b.desc, b.gs, torch.empty(0, 2, dtype=torch.int64, device="cuda"))
+    # sequences without new tokens, and contexts of length 0
+    b = Batch(152, W.F16, 4, 2, 64, 16, [0, 3, 0], [5, 0, 0])
+    before = b.gk.clone()
+    b.append()
+    out = b.prefill(0.1)
+    b.oracle_append()
+    H.assert_attention_close(H.out_to_double(out), b.attention(0.1), "one of three", W.F16)
+    same = torch.ones(b.nb, dtype=torch.bool)
+    same[int(b.tables[1, 0])] = False
+    assert torch.equal(before[same], b.gk[same])
+    assert int(b.err.item()) == 0
+
+
+def test_scaled_calls_with_a_bound_below_a_length():
+    """max_q_len smaller than a sequence's tokens: that sequence is flagged, its
+    rows are zero (prefill) or untouched (append), the others are right."""
+    b = Batch(153, W.F16, 4, 2, 64, 16, [300, 20], [0, 40])
+    before = (b.gk.clone(), b.gs.clone())
+    q_out = torch.full((320, 4, 64), 5.0, dtype=torch.float16, device="cuda")
+    b.max_new = 25
+    b.append(freqs(64), q_out=q_out)
+    assert int(b.err.item()) == B.PKV_DEVERR_CONTEXT and (q_out[:300] == 5).all()
+    own = torch.from_numpy(b.tables[0][b.tables[0] >= 0]).long().cuda()
+    assert torch.equal(before[0][own], b.gk[own])
+    check_rotated(q_out[300:], b.q[300:], OS.rotate(b.q, b.positions(), freqs(64))[300:], 1.0, W.F16, "q")
+    b.err.zero_()
+    out = b.prefill(0.1)
+    assert int(b.err.item()) == B.PKV_DEVERR_CONTEXT and (out[:300] == 0).all()
+    b.k, b.v, b.scales = (t.cpu().numpy() for t in (b.gk, b.gv, b.gs))
+    b.scales = np.where(np.isnan(b.scales), 1, b.scales)
+    ref = b.attention(0.1)
+    H.assert_attention_close(H.out_to_double(out)[300:], ref[300:], "bound", W.F16)
