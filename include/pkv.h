@@ -541,7 +541,8 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
  * pkv_paged_attention_decode.  pkv_decode_scaled_partition_size tells the choice
  * (0: equal shares), pkv_decode_scaled_workspace_bytes the scratch it needs.
  * A block with a bad id contributes nothing.  The same inputs and partition
- * size give the same bits on one kind of GPU.
+ * size give the same bits on one kind of GPU.  Calls that can overlap on the GPU
+ * need workspaces of their own.
  * Scales are positive and finite; V of a block loses no precision while its scale
  * is within 2^20 of the context's largest.
  * ------------------------------------------------------------------------- */

@@ -441,6 +441,15 @@ def _current_stream(t, name, stream):
     return _stream(stream)
 
 
+def _used_on(t, stream):
+    """A tensor that a call on an explicit stream allocates belongs to the current
+    stream: its memory must not be handed out again before that call is done."""
+    if stream is not None and t is not None:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        t.record_stream(torch.cuda.ExternalStream(handle))
+    return t
+
+
 def _i32(t, name):
     """Address of a dense int32 tensor."""
     if t.dtype is not _I32 or not t.is_contiguous():
@@ -485,7 +494,7 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     q (None without q).  `inv_freq` is a float64 device tensor of rot_dim / 2
     radians per position (rope.inv_freq computes it), or None to rotate
     nothing; with `scales` the cache is a scaled one."""
-    stream = _current_stream(k, "k", stream)
+    given, stream = stream, _current_stream(k, "k", stream)
     code = _code16(k, "k")
     rows, kv, d = shape = k.shape
     if kv != cache.num_kv_heads or d != cache.head_dim or v.shape != shape or \
@@ -499,7 +508,8 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
             raise ValueError("q must have the tokens, head_dim and type of k")
         qs = _token_rows(q, "q", rows, heads, d)
         if q_out is None:
-            q_out = torch.empty_like(q)        # (dense: q is, but for the space between tokens)
+            # (dense: q is, but for the space between tokens)
+            q_out = _used_on(torch.empty_like(q), given)
         else:
             _like(q_out, q, "q_out")
         qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -539,17 +549,17 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
                                       max_context_len, scale, partition_size=0, workspace=None,
                                       dev_err=None, out=None, stream=None):
     """Decode over a scaled cache; arguments as pkv_paged_attention_decode."""
-    stream = _current_stream(q, "q", stream)
+    given, stream = stream, _current_stream(q, "q", stream)
     s, h, d = q.shape
     n_tables, width = block_tables.shape
     if d != cache.head_dim or context_lens.numel() != s or n_tables != s or not q.is_contiguous():
         raise ValueError("q (dense), block_tables and context_lens do not fit together")
-    out = torch.empty_like(q) if out is None else _like(out, q, "out")
+    out = _used_on(torch.empty_like(q), given) if out is None else _like(out, q, "out")
     wp, ws_bytes = None, 0
     if workspace is None:
         need = pkv_decode_scaled_workspace_bytes(cache, s, h, max_context_len, partition_size)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _used_on(torch.empty(need, dtype=torch.uint8, device=q.device), given)
     if workspace is not None:
         wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = (_lib or load()).pkv_paged_attention_decode_scaled(
@@ -567,7 +577,7 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
                                        out=None, stream=None):
     """Causal attention over a scaled cache; arguments as
     pkv_paged_attention_prefill."""
-    stream = _current_stream(q, "q", stream)
+    given, stream = stream, _current_stream(q, "q", stream)
     total, h, d = q.shape
     num_seqs = context_lens.numel()
     n_tables, width = block_tables.shape
@@ -575,7 +585,7 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
             not q.is_contiguous():
         raise ValueError("q (dense), cu_seqlens_q, block_tables and context_lens do not fit "
                          "together")
-    out = torch.empty_like(q) if out is None else _like(out, q, "out")
+    out = _used_on(torch.empty_like(q), given) if out is None else _like(out, q, "out")
     st = (_lib or load()).pkv_paged_attention_prefill_scaled(
         ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), num_seqs, h,
         _i32(cu_seqlens_q, "cu_seqlens_q"), total, max_q_len, _i32(block_tables, "block_tables"),

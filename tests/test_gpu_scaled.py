@@ -788,3 +788,36 @@ def test_scaled_calls_with_a_bound_below_a_length():
     b.scales = np.where(np.isnan(b.scales), 1, b.scales)
     ref = b.attention(0.1)
     H.assert_attention_close(H.out_to_double(out)[300:], ref[300:], "bound", W.F16)
+
+
+def test_scaled_calls_on_an_explicit_stream():
+    """Calls that allocate their outputs and workspace, issued on a stream that is
+    not the current one, as an object and as a number, two at once."""
+    b = Batch(154, W.BF16, 8, 2, 64, 16, [1, 1, 1], [1500, 30, 1200])
+    b.oracle_append(freqs(64))
+    ref_q = OS.rotate(b.q, b.positions(), freqs(64))
+    f = torch.from_numpy(freqs(64)).cuda()
+    q, k, v = (b.dev16(x) for x in (b.q, b.nk, b.nv))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    caches = [(b.gk.clone(), b.gv.clone(), b.gs.clone()) for _ in streams]
+    got = []
+    for st, handle, (kc, vc, sc) in zip(streams, (streams[0], streams[1].cuda_stream), caches):
+        st.wait_stream(torch.cuda.current_stream())
+        d = B.cache_desc(kc, vc)
+        qr = B.pkv_rope_append(d, q, k, v, f, b.gcu, 1, b.gt, b.gctx, b.max_ctx, scales=sc,
+                               dev_err=b.err, stream=handle)
+        out = B.pkv_paged_attention_decode_scaled(d, sc, qr, b.gt, b.gctx, b.max_ctx, 0.125,
+                                                  dev_err=b.err, stream=handle)
+        pre = B.pkv_paged_attention_prefill_scaled(d, sc, qr, b.gcu, 1, b.gt, b.gctx, b.max_ctx,
+                                                   0.125, dev_err=b.err, stream=handle)
+        got.append((qr, out, pre))
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    check_rotated(got[0][0], b.q, ref_q, 1.0, W.BF16, "q")
+    b.k, b.v, b.scales = (t.cpu().numpy() for t in caches[0])
+    b.q = got[0][0].double().cpu().numpy()
+    for out in got[0][1:]:
+        H.assert_attention_close(H.out_to_double(out), b.attention(0.125), "stream", W.BF16)
