@@ -570,7 +570,10 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
  * with a bad id reads as zeros; a token that a row may not see does not reach
  * it, whatever its codes are.  A scale factor more than 2^22 below the largest
  * of the context rounds its block's values to 2^-41 of the largest value.
- * Device checks: as for the prefill.  Launches: one kernel.
+ * Device checks: as for the prefill.  Launches: one kernel; a CTA holds up to 256
+ * (token, query head) rows of a KV head and walks every key they see, so a few
+ * tokens after a long context (drafted ones, say) are better decoded, each as a
+ * sequence of its own with the same table row and its own length.
  * ------------------------------------------------------------------------- */
 pkv_status pkv_paged_attention_prefill_scaled(
     const pkv_cache_desc* cache, const float* scales, const void* q, int32_t q_dtype,

@@ -9,8 +9,8 @@
 // operands come about.  Four warpgroups share the registers by setmaxnreg:
 //   * warps 12-15 (load and convert): walk the block table, copy codes one slot
 //     ahead, turn them into fp16 and store them into the 128-byte-swizzled
-//     operand tiles of a ring, slot j = K(j) and V(j - 1).  A byte read once is written as two: codes
-//     cross HBM and L2 at half a 16-bit cache's traffic.
+//     operand tiles of a ring, slot j = K(j) and V(j - 1).  Codes cross HBM and
+//     L2 at half a 16-bit cache's traffic.
 //     The scale goes into the conversion: a block's K becomes code * (ks / kref)
 //     2^7 with kref a power of two at or above the CTA's largest ks (V alike),
 //     which fp16 holds exactly while the scales are powers of two within 2^22
