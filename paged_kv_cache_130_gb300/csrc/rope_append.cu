@@ -55,18 +55,18 @@ __device__ __forceinline__ float power_of_two(float bound)
 }
 
 // inv_freq (radians) as a 64-bit binary fraction of a turn: the 53-bit
-// significand times 2^65 / pi, shifted into place.  All in integers: this
-// GPU's fp64 units would take longer over a block's angles than its rows.
-__device__ __forceinline__ uint64_t turns_of(double inv_freq)
+// significand times 2^65 / pi = 2^66 / (2 pi) (`per_radian`), shifted into place.
+// All in integers: this GPU's fp64 units would take longer over a block's angles
+// than its rows.
+__device__ __forceinline__ uint64_t turns_of(double inv_freq, uint64_t per_radian)
 {
-    constexpr uint64_t kTurn = 0xa2f9836e4e441529ull;               // floor(2^65 / pi) = 2^66 / (2 pi)
     const uint64_t b = (uint64_t)__double_as_longlong(inv_freq);
     const int e = (int)(b >> 52) & 0x7ff;
     if (e == 0 || e > 1023 + 52)                       // zero and what is no frequency
         return 0;
     const uint64_t m = (b & 0xfffffffffffffull) | (1ull << 52);
-    const uint64_t lo = m * kTurn;
-    const uint64_t hi = __umul64hi(m, kTurn);
+    const uint64_t lo = m * per_radian;
+    const uint64_t hi = __umul64hi(m, per_radian);
     const int sh = 1077 - e;                           // >= 2
     const uint64_t t = sh >= 128 ? 0ull
                                  : (sh >= 64 ? hi >> (sh - 64) : (hi << (64 - sh)) | (lo >> sh));
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 
     // cosines and sines of the block's tokens
     for (int f = lane; f < rh; f += 32) {
-        const uint64_t turns = turns_of(__ldg(p.inv_freq + f));
+        const uint64_t turns = turns_of(__ldg(p.inv_freq + f), p.per_radian);
         // (set, frequency) = (f / 4, f % 4), or (f / 8, f % 8) in two fours
         float* at = sh_cs + (inter ? f : ((f >> 2) & 1) * (rh >> 1) + (f >> 3) * 4 + (f & 3));
         for (int t = warp; t < T; t += kWarps) {

@@ -196,6 +196,8 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
     p.rot_dim = rot_dim;
     p.interleaved = interleaved != 0;
     p.mscale = mscale;
+    static const uint64_t per_radian = (uint64_t)(ldexpl(1.0L, 65) / acosl(-1.0L));
+    p.per_radian = per_radian;
     p.k_bound = 1.f;
     if (rot_dim > 0 && 1.41421356f * fabsf(mscale) > 1.f)
         p.k_bound = 1.41421356f * fabsf(mscale);

@@ -30,6 +30,7 @@ struct RopeParams {
     int32_t rot_dim;
     int32_t interleaved;
     float mscale;
+    uint64_t per_radian;           // 2^65 / pi: 2^66ths of a turn in a radian
     float k_bound;                 // |rotated K| <= k_bound * max |K|
     int32_t num_seqs;
     const int32_t* cu_seqlens_q;
