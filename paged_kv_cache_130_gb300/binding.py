@@ -451,17 +451,19 @@ def _used_on(t, stream):
 
 
 def _i32(t, name):
-    """Address of a dense int32 tensor."""
-    if t.dtype is not _I32 or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32" % name)
+    """Address of a dense int32 tensor on the GPU."""
+    if t.dtype is not _I32 or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s must be contiguous int32 on the GPU" % name)
     return t.data_ptr()
 
 
-def _scales_of(cache, scales):
-    """Device address of a layer's scales, float32 [num_blocks, num_kv_heads, 2]."""
+def _scales_of(cache, scales, host_too=False):
+    """Address of a layer's scales, float32 [num_blocks, num_kv_heads, 2]."""
     if scales.dtype is not _F32 or not scales.is_contiguous() or \
-            scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads:
-        raise ValueError("scales must be contiguous float32 [num_blocks, num_kv_heads, 2]")
+            scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads or \
+            not (scales.is_cuda or host_too):
+        raise ValueError("scales must be contiguous float32 [num_blocks, num_kv_heads, 2] on the "
+                         "GPU")
     return scales.data_ptr()
 
 
@@ -482,7 +484,7 @@ def _token_rows(t, name, n, h, d):
 
 
 def _like(t, ref, name):
-    if t.shape != ref.shape or t.dtype is not ref.dtype or not t.is_contiguous():
+    if t.shape != ref.shape or t.dtype is not ref.dtype or not t.is_contiguous() or not t.is_cuda:
         raise ValueError("%s must be dense and like q" % name)
     return t
 
@@ -498,13 +500,13 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     code = _code16(k, "k")
     rows, kv, d = shape = k.shape
     if kv != cache.num_kv_heads or d != cache.head_dim or v.shape != shape or \
-            v.dtype is not k.dtype:
+            v.dtype is not k.dtype or not v.is_cuda:
         raise ValueError("k and v must be alike and fit the cache")
     qp = qo = None
     qs = heads = 0
     if q is not None:
         rows_q, heads, d_q = q.shape
-        if rows_q != rows or d_q != d or q.dtype is not k.dtype:
+        if rows_q != rows or d_q != d or q.dtype is not k.dtype or not q.is_cuda:
             raise ValueError("q must have the tokens, head_dim and type of k")
         qs = _token_rows(q, "q", rows, heads, d)
         if q_out is None:
@@ -515,8 +517,8 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
         qp, qo = q.data_ptr(), q_out.data_ptr()
     rot, fp = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype is not _F64 or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be contiguous float64")
+        if inv_freq.dtype is not _F64 or not inv_freq.is_contiguous() or not inv_freq.is_cuda:
+            raise ValueError("inv_freq must be contiguous float64 on the GPU")
         rot, fp = 2 * inv_freq.numel(), inv_freq.data_ptr()
     num_seqs = context_lens.numel()
     n_tables, width = block_tables.shape
@@ -561,6 +563,8 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
         if need > 0:
             workspace = _used_on(torch.empty(need, dtype=torch.uint8, device=q.device), given)
     if workspace is not None:
+        if not workspace.is_cuda:
+            raise ValueError("workspace must be on the GPU")
         wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = (_lib or load()).pkv_paged_attention_decode_scaled(
         ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), s, h,
@@ -612,11 +616,11 @@ def pkv_copy_blocks_scaled(caches, scales, block_pairs, dst=None, dst_scales=Non
         raise ValueError("block_pairs must be contiguous int64 [n, 2]")
     ptrs = ctypes.c_void_p * n
     a = (CacheDesc * n)(*caches)
-    a_s = ptrs(*[_scales_of(c, t) for c, t in zip(caches, scales)])
+    a_s = ptrs(*[_scales_of(c, t, dst is not None) for c, t in zip(caches, scales)])
     b = b_s = None
     if dst is not None:
         b = (CacheDesc * n)(*dst)
-        b_s = ptrs(*[_scales_of(c, t) for c, t in zip(dst, dst_scales)])
+        b_s = ptrs(*[_scales_of(c, t, True) for c, t in zip(dst, dst_scales)])
         stream = _stream(stream)
     else:
         stream = _current_stream(block_pairs, "block_pairs", stream)

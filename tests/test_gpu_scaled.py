@@ -821,3 +821,29 @@ def test_scaled_calls_on_an_explicit_stream():
     b.q = got[0][0].double().cpu().numpy()
     for out in got[0][1:]:
         H.assert_attention_close(H.out_to_double(out), b.attention(0.125), "stream", W.BF16)
+
+
+def test_scaled_calls_refuse_host_tensors():
+    """Every tensor has to be on the GPU: a host address would be read there."""
+    b = Batch(155, W.F16, 4, 2, 64, 16, [1, 1], [20, 5])
+    f = torch.from_numpy(freqs(64)).cuda()
+    good = dict(q=b.dev16(b.q), k=b.dev16(b.nk), v=b.dev16(b.nv), inv_freq=f, cu_seqlens_q=b.gcu,
+                block_tables=b.gt, context_lens=b.gctx, scales=b.gs,
+                q_out=torch.empty(2, 4, 64, dtype=torch.float16, device="cuda"))
+    for name in good:
+        with pytest.raises(ValueError):
+            B.pkv_rope_append(b.desc, max_q_len=1, max_context_len=21, **dict(good, **{name: good[name].cpu()}))
+    args = dict(scales=b.gs, q=good["q"], block_tables=b.gt, context_lens=b.gctx, out=good["q_out"])
+    for name in args:
+        with pytest.raises(ValueError):
+            B.pkv_paged_attention_decode_scaled(b.desc, max_context_len=21, scale=0.1,
+                                                **dict(args, **{name: args[name].cpu()}))
+    args["cu_seqlens_q"] = b.gcu
+    for name in args:
+        with pytest.raises(ValueError):
+            B.pkv_paged_attention_prefill_scaled(b.desc, max_q_len=1, max_context_len=21, scale=0.1,
+                                                 **dict(args, **{name: args[name].cpu()}))
+    pairs = torch.tensor([[0, 1]])
+    for p, s in ((pairs, b.gs), (pairs.cuda(), b.gs.cpu())):
+        with pytest.raises(ValueError):
+            B.pkv_copy_blocks_scaled(b.desc, s, p)
