@@ -20,8 +20,12 @@
 //   * warps 8 and 10 (one issuing thread each): O_w += P_w(j-1) V(j-1), then
 //     S_w(j) = Q_w K(j)^T, taking turns by slot.
 //   * warps 0-3 and 4-7: softmax, one thread per row.  q is fp16 per row times
-//     a power of two (bf16 values fit without loss); the weights are fp16 (11
-//     bits, 2^-12 relative at most), so P V is one product for both types.
+//     a power of two (bf16 values fit without loss); the weights are fp16, so
+//     P V is one product for both types: each is off by at most 2^-11 of itself,
+//     or by 2^-31 where it is a subnormal.  For that they are stored times 2^6
+//     (at most 2^14 with the maximum's lag of 2^8), which the sums carry too and
+//     O / l leaves out; at 2^0 a flat tail 2^-25 below one large weight, however
+//     long, became nothing.
 // NaN codes of V: a weight of 0 times NaN would reach rows that may not see the
 // token, so the converter stores 0 and notes the first position of a NaN per
 // output column; rows at or past it get NaN there.
@@ -61,6 +65,8 @@ static_assert(2 * kSoftmaxRegs + kMmaRegs + kConvRegs <= 4 * kLaunchRegs, "regis
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kBatch = 4;             // vectors a converting lane has in hand
 constexpr float kUnit = 128.f;         // fp16 value of a code at the reference scale
+constexpr float kRaise = 8.f;          // log2: how far a score may pass the running maximum
+constexpr float kWeightExp = 6.f;      // log2 of the weight at the running maximum
 
 template <int D>
 struct Layout {
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mx = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]),
                                        fmaxf(mc[6], mc[7]));
                 const float m_cand = fmaxf(m_run, mx * qk);
-                const bool raise = m_cand > m_run + 8.f;
+                const bool raise = m_cand > m_run + kRaise;
                 const float m_new = raise ? m_cand : m_run;
                 const float alpha = raise ? fast_exp2(m_run - m_new) : 1.f;   // 0 on the first tile
                 if (kt > 0 && __any_sync(0xffffffffu, raise)) {
@@ -571,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 m_run = m_new;
                 const float2 qk2 = make_float2(qk, qk);
-                const float2 nm2 = make_float2(-m_new, -m_new);
+                const float2 nm2 = make_float2(kWeightExp - m_new, kWeightExp - m_new);
                 float2 ls[4] = {};                     // four pairs of partial sums
                 // P over S: 16 keys as 8 columns of fp16 pairs at the start of
                 // those keys' own 16 columns
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t hi[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        // exp2(s qk - m); a masked key (-inf) gives 0
+                        // 2^6 exp2(s qk - m); a masked key (-inf) gives 0
                         const float2 t = ffma2(make_float2(x[c0 + 2 * e], x[c0 + 2 * e + 1]), qk2, nm2);
                         const float2 pp = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                         ls[e & 3] = fadd2(ls[e & 3], pp);
