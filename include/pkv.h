@@ -568,8 +568,11 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
  * pkv_paged_attention_prefill with k_t and v_t = code * scale of their block and
  * KV head.  q and out F16 or BF16, 1..128 query heads per KV head.  A block
  * with a bad id reads as zeros; a token that a row may not see does not reach
- * it, whatever its codes are.  A scale factor more than 2^22 below the largest
- * of the context rounds its block's values to 2^-41 of the largest value.
+ * it, whatever its codes are.  Scales are positive, normal and finite, of any
+ * value; powers of two, as pkv_rope_append writes them, are up to a quarter
+ * faster.  Codes of a block whose scale is more than 2^22 below the largest of
+ * the context are off by up to 2^-31 of that scale.  Weights are rounded to fp16:
+ * by 2^-11 of themselves at most, or 2^-31 of the row's largest.
  * Device checks: as for the prefill.  Launches: one kernel; a CTA holds up to 256
  * (token, query head) rows of a KV head and walks every key they see, so a few
  * tokens after a long context (drafted ones, say) are better decoded, each as a

@@ -11,12 +11,16 @@
 //     ahead, turn them into fp16 and store them into the 128-byte-swizzled
 //     operand tiles of a ring, slot j = K(j) and V(j - 1).  Codes cross HBM and
 //     L2 at half a 16-bit cache's traffic.
-//     The scale goes into the conversion: a block's K becomes code * (ks / kref)
-//     2^7 with kref a power of two at or above the CTA's largest ks (V alike),
-//     which fp16 holds exactly while the scales are powers of two within 2^22
-//     of the largest; what falls below is under 2^-41 of the largest value.
-//     So one factor serves all scores, one all outputs, and the softmax does
-//     not know about blocks.
+//     The scale's power of two goes into the conversion: a block's K becomes
+//     code * 2^(e - eref + 7) with 2^eref the power of two of the CTA's largest
+//     ks (V alike), which fp16 holds exactly down to 2^-22 of the largest; what
+//     a block further down loses is at most 2^-32 of the largest scale.  So one
+//     factor serves all scores, one all outputs, and while the scales are powers
+//     of two, as the append makes them, the softmax does not know about blocks.
+//     Otherwise the rest of each scale, in [1, 2), multiplies its block's scores
+//     and weights there, in fp32 (rounding it into the fp16 factor moved all
+//     scores of a block by up to 2^-11); chunks then take 281 us instead of 227,
+//     prompts 198 instead of 175.
 //   * warps 8 and 10 (one issuing thread each): O_w += P_w(j-1) V(j-1), then
 //     S_w(j) = Q_w K(j)^T, taking turns by slot.
 //   * warps 0-3 and 4-7: softmax, one thread per row.  q is fp16 per row times
@@ -41,6 +45,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "pkv_common.cuh"
 #include "scaled_internal.h"
@@ -144,13 +150,22 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* fl
     return ok;
 }
 
-// A power of two at or above every scale up to the one whose bits these are.
+// A normal scale = power_of(scale) * rest_of(scale), a power of two and a number
+// in [1, 2).
+__device__ __forceinline__ float power_of(float scale)
+{
+    return __uint_as_float(__float_as_uint(scale) & 0x7f800000u);
+}
+__device__ __forceinline__ float rest_of(float scale)
+{
+    return __uint_as_float((__float_as_uint(scale) & 0x007fffffu) | 0x3f800000u);
+}
+
+// The power of two of the scale whose bits these are, a normal number.
 __device__ __forceinline__ float reference_of(const uint32_t* bits)
 {
     const uint32_t e = *reinterpret_cast<const volatile uint32_t*>(bits) & 0x7f800000u;
-    if (e == 0)
-        return 1.1754944e-38f;
-    return e >= 0x7e800000u ? 1.7014118e38f : __uint_as_float(e + 0x00800000u);
+    return __uint_as_float(min(max(e, 0x00800000u), 0x7f000000u));
 }
 
 // code * f for 16 codes, as 16 fp16 values (f: the factor in both halves).
@@ -231,14 +246,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int CT = QT_;                    // type of q and out
     constexpr int ST = L::ST;
     constexpr int NB = kKeys / BS;             // blocks per K/V tile
+    // tiles whose scales' rests are kept: the converting warps write tile j's once
+    // slot j - ST is free, so tile j - ST may still be in the softmax
+    constexpr int NR = ST < 4 ? 4 : 8;
+    static_assert(NR > ST && (NR & (NR - 1)) == 0, "ring of the rests");
     const PrefillParams& p = sp.p;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) Bars<ST> bars;
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     __shared__ uint32_t ref_bits[2];           // largest ks, vs of the CTA's blocks
+    __shared__ int any_rest;                   // some scale is no power of two
+    __shared__ float rests[NR][2][NB];         // then: the rests of ks, vs by tile
     __shared__ int nan_pos[D];                 // first key whose V is NaN in this column
     __shared__ int any_nan;
+    __shared__ int64_t first_rows[2];          // where the query tiles' outputs start
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -318,6 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_flag = 0;
         any_nan = 0;
+        any_rest = 0;
+        first_rows[0] = row_off(j0, 0);
+        first_rows[1] = row_off(j0 + QT, 0);
         ref_bits[0] = ref_bits[1] = 0u;
     }
     if (tid < D)
@@ -425,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         uint32_t mk = sc_first.x > 0.f ? __float_as_uint(sc_first.x) : 0u;
         uint32_t mv = sc_first.y > 0.f ? __float_as_uint(sc_first.y) : 0u;
+        uint32_t rest = mk | mv;
         for (int b = tid + kThreads; b < nblocks; b += kThreads) {
             const int phys = __ldg(table + b);
             if (!block_ok(phys)) {
@@ -432,10 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             const float2 sc = __ldg(scales + (int64_t)phys * p.num_kv_heads + g);
-            if (sc.x > 0.f)
-                mk = max(mk, __float_as_uint(sc.x));
-            if (sc.y > 0.f)
-                mv = max(mv, __float_as_uint(sc.y));
+            const uint32_t ks = sc.x > 0.f ? __float_as_uint(sc.x) : 0u;
+            const uint32_t vs = sc.y > 0.f ? __float_as_uint(sc.y) : 0u;
+            mk = max(mk, ks);
+            mv = max(mv, vs);
+            rest |= ks | vs;
         }
         mk = __reduce_max_sync(0xffffffffu, mk);
         mv = __reduce_max_sync(0xffffffffu, mv);
@@ -443,6 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicMax(&ref_bits[0], mk);
             atomicMax(&ref_bits[1], mv);
         }
+        if (rest & 0x007fffffu)
+            *reinterpret_cast<volatile int*>(&any_rest) = 1;
     }
     // The converting warps wait for everybody's part; the others read the maxima
     // when the first slot, which those warps fill, has come to them.
@@ -516,18 +545,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = pos0 + r / G;              // this row's position
             float m_run = kNegInf;                     // running max of the scaled logits
             float l_run = 0.f;
-            bool alive = true;
+            // The tiles' loop has two forms that differ in the rests of the scales
+            // only: with a branch for them inside one loop the chunks took 239-264
+            // us instead of 227.  (Its body keeps the loop's own indentation.)
+            bool alive = wait_warp(s_addr(&bars.s_full[w]), 0, &abort_flag, p.dev_err);
+            // K's reference and the kind of the scales come with the first keys.
+            // (The factor is at least 1e-30, where the scores of such small keys
+            // vanish all the same: 0 times a masked key's -inf would be NaN.)
+            qk = fmaxf(qk * reference_of(&ref_bits[0]), 1e-30f);
+            auto tiles = [&](auto with_rests) {
+            constexpr bool kRests = decltype(with_rests)::value;
             for (int kt = 0; kt < nkv; ++kt) {
-                if (!wait_warp(s_addr(&bars.s_full[w]), kt & 1, &abort_flag, p.dev_err)) {
+                if (kt > 0 && !wait_warp(s_addr(&bars.s_full[w]), kt & 1, &abort_flag, p.dev_err)) {
                     alive = false;
                     break;
                 }
                 tc_fence_after();
-                // K's reference, with the first keys.  (At least 1e-30, where the
-                // scores of such small keys vanish all the same: 0 times a masked
-                // key's -inf would be NaN.)
-                if (kt == 0)
-                    qk = fmaxf(qk * reference_of(&ref_bits[0]), 1e-30f);
                 float x[kKeys];
 #pragma unroll
                 for (int c0 = 0; c0 < kKeys; c0 += 16)
@@ -543,6 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             x[j0 + j] = (bits >> j) & 1u ? x[j0 + j] : kNegInf;
+                    }
+                }
+                [[maybe_unused]] const volatile float* rest = &rests[kt & (NR - 1)][0][0];
+                if constexpr (kRests) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const float f = rest[b];
+#pragma unroll
+                        for (int j = 0; j < BS; ++j)
+                            x[b * BS + j] *= f;
                     }
                 }
                 // row max: eight independent chains of three-input maxima
@@ -588,8 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 8; ++e) {
                         // 2^6 exp2(s qk - m); a masked key (-inf) gives 0
                         const float2 t = ffma2(make_float2(x[c0 + 2 * e], x[c0 + 2 * e + 1]), qk2, nm2);
-                        const float2 pp = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                        float2 pp = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                         ls[e & 3] = fadd2(ls[e & 3], pp);
+                        if constexpr (kRests) {
+                            const float f = rest[NB + (c0 + 2 * e) / BS];
+                            pp.x *= f, pp.y *= f;
+                        }
                         hi[e] = pack_rn<kF16>(pp.x, pp.y);
                     }
                     tmem_st8(t_s + c0, hi);
@@ -606,6 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l_run = l_run * alpha + lsum;
                 tc_fence_before();
                 bar_arrive(s_addr(&bars.p_full[w]));
+            }
+            };
+            if (alive) {
+                if (__builtin_expect(*reinterpret_cast<volatile int*>(&any_rest) == 0, 1))
+                    tiles(std::false_type{});
+                else
+                    tiles(std::true_type{});
             }
             if (alive)
                 alive = wait_warp(s_addr(&bars.o_full[w]), 0, &abort_flag, p.dev_err);
@@ -645,6 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          : "memory");
                 }
                 __syncwarp();
+                // (kept in shared memory meanwhile: a register spilled around the
+                // loop above comes back from L2, which cost the prompts 5 %)
+                const int64_t first_row = *reinterpret_cast<volatile int64_t*>(&first_rows[w]);
                 const int c = lane % LPR;
 #pragma unroll 4
                 for (int i = 0; i < NA; ++i) {
@@ -742,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (the references are powers of two: their inverses are exact)
         const float kinv = 1.f / reference_of(&ref_bits[0]), vinv = 1.f / reference_of(&ref_bits[1]);
         auto factor = [&](float sc, float inv) -> uint32_t {
-            const float f = sc * inv * kUnit;
+            const float f = power_of(sc) * inv * kUnit;
             return pack_rn<kF16>(f, f);
         };
         // convert vectors i0 ..., with their blocks' factors, into their places of
@@ -767,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared16(dst + place1 + at, hi[u]);
             }
         };
+        const bool uneven = *reinterpret_cast<volatile int*>(&any_rest) != 0;
         float2 sc0 = scales_of(id0), sc1 = scales_of(id1);
         uint32_t fv = 0u;                                          // V's factor of tile j - 1
         for (int j = 0; j <= nk; ++j) {
@@ -778,6 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_warp(s_addr(&bars.empty[st]), ((j / ST) & 1) ^ 1, &abort_flag, p.dev_err))
                 break;
             const uint32_t dst = sb + L::slot + st * L::SLOT;
+            if (uneven && j < nk && cw == 0 && lane < NB) {
+                rests[j & (NR - 1)][0][lane] = rest_of(sc0.x);
+                rests[j & (NR - 1)][1][lane] = rest_of(sc0.y);
+            }
             // each place is refilled for the next slot once its codes are used
             if (j < nk) {
 #pragma unroll
