@@ -142,6 +142,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _allocate(make, stream):
+    """make(), a tensor that a call on `stream` writes.  With an explicit stream it
+    comes from that stream's pool: memory from the current stream's may still be
+    read there, by work queued before its last owner let go of it, and the call
+    does not wait for that.  The caller reads the tensor on the current stream, so
+    its memory is not handed out again before that stream is done either."""
+    if stream is None:
+        return make()
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
+        t = make()
+    if here.cuda_stream != handle:
+        t.record_stream(here)
+    return t
+
+
 def _check(status, where):
     if status != PKV_OK:
         raise PkvError(status, where)
@@ -441,15 +458,6 @@ def _current_stream(t, name, stream):
     return _stream(stream)
 
 
-def _used_on(t, stream):
-    """A tensor that a call on an explicit stream allocates belongs to the current
-    stream: its memory must not be handed out again before that call is done."""
-    if stream is not None and t is not None:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        t.record_stream(torch.cuda.ExternalStream(handle))
-    return t
-
-
 def _i32(t, name):
     """Address of a dense int32 tensor on the GPU."""
     if t.dtype is not _I32 or not t.is_contiguous() or not t.is_cuda:
@@ -511,7 +519,7 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
         qs = _token_rows(q, "q", rows, heads, d)
         if q_out is None:
             # (dense: q is, but for the space between tokens)
-            q_out = _used_on(torch.empty_like(q), given)
+            q_out = _allocate(lambda: torch.empty_like(q), given)
         else:
             _like(q_out, q, "q_out")
         qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -556,12 +564,13 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
     n_tables, width = block_tables.shape
     if d != cache.head_dim or context_lens.numel() != s or n_tables != s or not q.is_contiguous():
         raise ValueError("q (dense), block_tables and context_lens do not fit together")
-    out = _used_on(torch.empty_like(q), given) if out is None else _like(out, q, "out")
+    out = _allocate(lambda: torch.empty_like(q), given) if out is None else _like(out, q, "out")
     wp, ws_bytes = None, 0
     if workspace is None:
         need = pkv_decode_scaled_workspace_bytes(cache, s, h, max_context_len, partition_size)
         if need > 0:
-            workspace = _used_on(torch.empty(need, dtype=torch.uint8, device=q.device), given)
+            workspace = _allocate(
+                lambda: torch.empty(need, dtype=torch.uint8, device=q.device), given)
     if workspace is not None:
         if not workspace.is_cuda:
             raise ValueError("workspace must be on the GPU")
@@ -589,7 +598,7 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
             not q.is_contiguous():
         raise ValueError("q (dense), cu_seqlens_q, block_tables and context_lens do not fit "
                          "together")
-    out = _used_on(torch.empty_like(q), given) if out is None else _like(out, q, "out")
+    out = _allocate(lambda: torch.empty_like(q), given) if out is None else _like(out, q, "out")
     st = (_lib or load()).pkv_paged_attention_prefill_scaled(
         ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), num_seqs, h,
         _i32(cu_seqlens_q, "cu_seqlens_q"), total, max_q_len, _i32(block_tables, "block_tables"),

@@ -1,0 +1,111 @@
+"""How the scaled-cache calls and the rotary append treat what surrounds them:
+streams, memory they allocate, and arguments they refuse."""
+import pytest
+import torch
+
+import harness as H
+from test_gpu_scaled import Batch, freqs
+
+from paged_kv_cache_130_gb300 import binding as B
+from paged_kv_cache_130_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    H.build_library()
+
+
+def pool_of(address):
+    """Handle of the stream whose memory pool holds an address."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= address < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not torch's memory")
+
+
+def scaled_calls(b, f, stream):
+    """Every call that allocates, on `stream`: name -> a function that makes it."""
+    q, k, v = (b.dev16(x) for x in (b.q, b.nk, b.nv))
+    kw = dict(dev_err=b.err, stream=stream)
+    return dict(
+        rope=lambda: B.pkv_rope_append(b.desc, q, k, v, f, b.gcu, b.max_new, b.gt, b.gctx,
+                                       b.max_ctx, scales=b.gs, **kw),
+        decode=lambda: B.pkv_paged_attention_decode_scaled(b.desc, b.gs, q, b.gt, b.gctx,
+                                                           b.max_ctx, 0.125, **kw),
+        prefill=lambda: B.pkv_paged_attention_prefill_scaled(b.desc, b.gs, q, b.gcu, b.max_new,
+                                                             b.gt, b.gctx, b.max_ctx, 0.125, **kw))
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_what_a_call_on_another_stream_allocates_is_that_streams(as_number, monkeypatch):
+    """Outputs and workspace come from the pool of the stream they are written
+    on: a block of the current stream's could still be read there."""
+    b = Batch(300, W.BF16, 8, 2, 64, 16, [1, 1, 1], [1500, 30, 1200])
+    f = torch.from_numpy(freqs(64)).cuda()
+    side = torch.cuda.Stream()
+    calls = scaled_calls(b, f, side.cuda_stream if as_number else side)
+    torch.cuda.synchronize()
+    made = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(empty(*a, **k)) or made[-1])
+    for name, call in calls.items():
+        out = call()
+        assert pool_of(out.data_ptr()) == side.cuda_stream, name
+        torch.cuda.synchronize()
+    assert made and all(pool_of(t.data_ptr()) == side.cuda_stream for t in made)
+    assert int(b.err.item()) == 0
+
+
+def test_a_call_on_another_stream_leaves_memory_in_use_alone():
+    """The current stream is busy and then reads tensors that their owner has let
+    go of; calls on another stream that could get that memory must not write it."""
+    b = Batch(301, W.BF16, 8, 2, 64, 16, [1, 1, 1], [1500, 30, 1200])
+    f = torch.from_numpy(freqs(64)).cuda()
+    side = torch.cuda.Stream()
+    calls = scaled_calls(b, f, side)
+    torch.cuda.synchronize()
+    like = calls["decode"]()
+    calls["prefill"]()
+    torch.cuda.synchronize()
+    for name in ("decode", "prefill"):
+        xs = [torch.full_like(like, float(i)) for i in range(8)]
+        ys = [torch.empty_like(like) for _ in xs]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)                       # ~10 ms
+        for x, y in zip(xs, ys):
+            y.copy_(x)
+        del x, xs
+        outs = [calls[name]() for _ in range(8)]
+        torch.cuda.synchronize()
+        assert all((y == i).all() for i, y in enumerate(ys))
+        # (bits: the last token's K and V are not written, and read as NaN)
+        bits = [o.view(torch.int16) for o in outs]
+        assert all(torch.equal(x, bits[0]) for x in bits)
+
+
+def test_calls_on_another_stream_in_a_captured_graph():
+    """A capture that forks to another stream and joins it again."""
+    b = Batch(302, W.BF16, 8, 2, 64, 16, [1, 1, 1], [1500, 30, 1200])
+    b.oracle_append()
+    b.upload()
+    f = torch.from_numpy(freqs(64)).cuda()
+    side = torch.cuda.Stream()
+    calls = scaled_calls(b, f, side)
+    side.wait_stream(torch.cuda.current_stream())
+    want = [calls[n]() for n in ("decode", "prefill")]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [calls[n]() for n in ("decode", "prefill")]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, got))
+    assert int(b.err.item()) == 0
