@@ -230,10 +230,11 @@ def _decode_common(fn, where, cache, q, block_tables, context_lens, max_context_
         raise ValueError("block_tables and context_lens must be int32")
     s, h, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocate(lambda: torch.empty_like(q), stream)
     need = pkv_decode_workspace_bytes(cache, s, h, max_context_len, partition_size)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(lambda: torch.empty(need, dtype=torch.uint8, device=q.device),
+                              stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(fn(ctypes.byref(cache), _ptr(q), dtype_code(q.dtype), s, h, _ptr(block_tables),
               block_tables.shape[1], _ptr(context_lens), int(max_context_len), float(scale),
@@ -284,7 +285,7 @@ def pkv_paged_attention_decode_static_ws(cache, q, block_tables, context_lens, m
         raise ValueError("block_tables and context_lens must be int32")
     s, h, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocate(lambda: torch.empty_like(q), stream)
     _check(load().pkv_paged_attention_decode_static_ws(
         ctypes.byref(cache), _ptr(q), dtype_code(q.dtype), s, h, _ptr(block_tables),
         block_tables.shape[1], _ptr(context_lens), int(max_context_len), float(scale),
@@ -339,10 +340,11 @@ def pkv_paged_attention_decode_shared_prefix(cache, q, block_tables, context_len
         raise ValueError("group_begin needs num_groups + 1 entries")
     s, h, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocate(lambda: torch.empty_like(q), stream)
     need = pkv_shared_prefix_workspace_bytes(cache, s, h, max_context_len, partition_size)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(lambda: torch.empty(need, dtype=torch.uint8, device=q.device),
+                              stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().pkv_paged_attention_decode_shared_prefix(
         ctypes.byref(cache), _ptr(q), dtype_code(q.dtype), s, h, _ptr(block_tables),
@@ -368,7 +370,7 @@ def pkv_paged_attention_prefill(cache, q, cu_seqlens_q, max_q_len, block_tables,
     if cu_seqlens_q.numel() != num_seqs + 1:
         raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocate(lambda: torch.empty_like(q), stream)
     _check(load().pkv_paged_attention_prefill(
         ctypes.byref(cache), _ptr(q), dtype_code(q.dtype), num_seqs, h, _ptr(cu_seqlens_q),
         total, int(max_q_len), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
@@ -418,14 +420,18 @@ def pkv_block_hashes(token_ids, cu_seqlens, block_size, block_offsets=None, pare
         full = torch.diff(cu_seqlens.to(torch.int64)) // block_size
         block_offsets = torch.cumsum(full, 0) - full
         total_blocks = int(full.sum().item())
+        if stream is not None:
+            # (read there after the caller's view of it is gone)
+            block_offsets.record_stream(torch.cuda.ExternalStream(
+                stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
     else:
         _dense(block_offsets, "block_offsets")
         total_blocks = hashes.shape[0] if hashes is not None else None
         if total_blocks is None:
             raise ValueError("pass `hashes` together with `block_offsets`")
     if hashes is None:
-        hashes = torch.empty((max(total_blocks, 1), 32), dtype=torch.uint8,
-                             device=token_ids.device)
+        hashes = _allocate(lambda: torch.empty((max(total_blocks, 1), 32), dtype=torch.uint8,
+                                               device=token_ids.device), stream)
     if parent_hashes is not None:
         _dense(parent_hashes, "parent_hashes")
     _check(load().pkv_block_hashes(_ptr(token_ids), _ptr(cu_seqlens), num_seqs,
