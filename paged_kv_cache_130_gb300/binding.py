@@ -41,6 +41,7 @@ class CacheDesc(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("cache_dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+    device = None          # of the caches (-1: host), where cache_desc made it
 
 
 _lib = None
@@ -174,11 +175,14 @@ def cache_desc(k_cache, v_cache, k_scale=1.0, v_scale=1.0):
     """Descriptor of one layer's caches, each [num_blocks, num_kv_heads, block_size, head_dim]."""
     _dense(k_cache, "k_cache")
     _dense(v_cache, "v_cache")
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4:
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4 or \
+            k_cache.device != v_cache.device:
         raise ValueError("k_cache and v_cache must be alike, 4-D")
     nb, hkv, bs, d = k_cache.shape
-    return CacheDesc(k_cache.data_ptr(), v_cache.data_ptr(), nb, hkv, bs, d,
+    desc = CacheDesc(k_cache.data_ptr(), v_cache.data_ptr(), nb, hkv, bs, d,
                      dtype_code(k_cache.dtype), float(k_scale), float(v_scale))
+    desc.device = k_cache.get_device()
+    return desc
 
 
 # ------------------------------------------------------------------ entry points
@@ -451,33 +455,53 @@ _I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 _CODES = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
 
 
-def _current_stream(t, name, stream):
-    """The stream's handle; t must be on the current device, where a call runs."""
-    if _raw_stream is not None and _raw_device is not None:
-        i = _raw_device() if t.get_device() >= 0 else -2
-        if t.get_device() != i:
-            raise ValueError("%s must be on the current CUDA device" % name)
-        if stream is None:
-            return _raw_stream(i)
-    elif not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _here(t, name):
+    """The current CUDA device, where a call runs; t must be on it."""
+    dev = t.get_device()
+    if dev < 0 or dev != (_raw_device() if _raw_device is not None else
+                          torch.cuda.current_device()):
         raise ValueError("%s must be on the current CUDA device" % name)
+    return dev
+
+
+def _handle(stream, dev):
+    """Handle of `stream`, or of device dev's current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
     return _stream(stream)
 
 
-def _i32(t, name):
-    """Address of a dense int32 tensor on the GPU."""
-    if t.dtype is not _I32 or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("%s must be contiguous int32 on the GPU" % name)
+def _refuse(t, dev, name, what):
+    """The error of a tensor that is not `what` on device dev."""
+    if t.get_device() != dev:
+        what = "on the current CUDA device"
+    return ValueError("%s must be %s" % (name, what))
+
+
+def _elsewhere(cache, dev):
+    """Whether cache_desc made it on another device than dev."""
+    return cache.device != dev and cache.device is not None
+
+
+def _i32(t, name, dev):
+    """Address of a dense int32 tensor on device dev."""
+    if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
+        raise _refuse(t, dev, name, "contiguous int32")
     return t.data_ptr()
 
 
-def _scales_of(cache, scales, host_too=False):
+def _err_flag(t, dev):
+    """Address of the word that device checks set bits in."""
+    if t.dtype is not _I32 or t.numel() < 1 or t.get_device() != dev:
+        raise _refuse(t, dev, "dev_err", "int32 with an element")
+    return t.data_ptr()
+
+
+def _scales_of(cache, scales, dev):
     """Address of a layer's scales, float32 [num_blocks, num_kv_heads, 2]."""
-    if scales.dtype is not _F32 or not scales.is_contiguous() or \
-            scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads or \
-            not (scales.is_cuda or host_too):
-        raise ValueError("scales must be contiguous float32 [num_blocks, num_kv_heads, 2] on the "
-                         "GPU")
+    if scales.dtype is not _F32 or not scales.is_contiguous() or scales.get_device() != dev or \
+            scales.numel() != 2 * cache.num_blocks * cache.num_kv_heads:
+        raise _refuse(scales, dev, "scales", "contiguous float32 [num_blocks, num_kv_heads, 2]")
     return scales.data_ptr()
 
 
@@ -497,9 +521,10 @@ def _token_rows(t, name, n, h, d):
     return a if n > 1 else h * d
 
 
-def _like(t, ref, name):
-    if t.shape != ref.shape or t.dtype is not ref.dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("%s must be dense and like q" % name)
+def _like(t, ref, name, dev):
+    if t.shape != ref.shape or t.dtype is not ref.dtype or not t.is_contiguous() or \
+            t.get_device() != dev:
+        raise _refuse(t, dev, name, "dense and like q")
     return t
 
 
@@ -510,41 +535,48 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     q (None without q).  `inv_freq` is a float64 device tensor of rot_dim / 2
     radians per position (rope.inv_freq computes it), or None to rotate
     nothing; with `scales` the cache is a scaled one."""
-    given, stream = stream, _current_stream(k, "k", stream)
+    dev = _here(k, "k")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
     code = _code16(k, "k")
     rows, kv, d = shape = k.shape
     if kv != cache.num_kv_heads or d != cache.head_dim or v.shape != shape or \
-            v.dtype is not k.dtype or not v.is_cuda:
+            v.dtype is not k.dtype:
         raise ValueError("k and v must be alike and fit the cache")
+    if v.get_device() != dev:
+        raise _refuse(v, dev, "v", "")
     qp = qo = None
     qs = heads = 0
     if q is not None:
         rows_q, heads, d_q = q.shape
-        if rows_q != rows or d_q != d or q.dtype is not k.dtype or not q.is_cuda:
-            raise ValueError("q must have the tokens, head_dim and type of k")
+        if rows_q != rows or d_q != d or q.dtype is not k.dtype or q.get_device() != dev:
+            raise _refuse(q, dev, "q", "alike k in its tokens, head_dim and type")
         qs = _token_rows(q, "q", rows, heads, d)
         if q_out is None:
             # (dense: q is, but for the space between tokens)
-            q_out = _allocate(lambda: torch.empty_like(q), given)
+            q_out = torch.empty_like(q) if stream is None else \
+                _allocate(lambda: torch.empty_like(q), stream)
         else:
-            _like(q_out, q, "q_out")
+            _like(q_out, q, "q_out", dev)
         qp, qo = q.data_ptr(), q_out.data_ptr()
     rot, fp = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype is not _F64 or not inv_freq.is_contiguous() or not inv_freq.is_cuda:
-            raise ValueError("inv_freq must be contiguous float64 on the GPU")
+        if inv_freq.dtype is not _F64 or not inv_freq.is_contiguous() or \
+                inv_freq.get_device() != dev:
+            raise _refuse(inv_freq, dev, "inv_freq", "contiguous float64")
         rot, fp = 2 * inv_freq.numel(), inv_freq.data_ptr()
     num_seqs = context_lens.numel()
     n_tables, width = block_tables.shape
     if cu_seqlens_q.numel() != num_seqs + 1 or n_tables != num_seqs:
         raise ValueError("cu_seqlens_q needs num_seqs + 1 entries, block_tables num_seqs rows")
     st = (_lib or load()).pkv_rope_append(
-        ctypes.byref(cache), None if scales is None else _scales_of(cache, scales), qp, qs,
+        ctypes.byref(cache), None if scales is None else _scales_of(cache, scales, dev), qp, qs,
         k.data_ptr(), _token_rows(k, "k", rows, kv, d), v.data_ptr(),
         _token_rows(v, "v", rows, kv, d), code, heads, fp, rot, interleaved, mscale, num_seqs,
-        _i32(cu_seqlens_q, "cu_seqlens_q"), rows, max_q_len, _i32(block_tables, "block_tables"),
-        width, _i32(context_lens, "context_lens"), max_context_len,
-        None if dev_err is None else dev_err.data_ptr(), qo, stream)
+        _i32(cu_seqlens_q, "cu_seqlens_q", dev), rows, max_q_len,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
+        max_context_len, None if dev_err is None else _err_flag(dev_err, dev), qo,
+        _handle(stream, dev))
     if st:
         raise PkvError(st, "pkv_rope_append")
     return q_out if q is not None else None
@@ -565,27 +597,35 @@ def pkv_paged_attention_decode_scaled(cache, scales, q, block_tables, context_le
                                       max_context_len, scale, partition_size=0, workspace=None,
                                       dev_err=None, out=None, stream=None):
     """Decode over a scaled cache; arguments as pkv_paged_attention_decode."""
-    given, stream = stream, _current_stream(q, "q", stream)
+    dev = _here(q, "q")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
     s, h, d = q.shape
     n_tables, width = block_tables.shape
     if d != cache.head_dim or context_lens.numel() != s or n_tables != s or not q.is_contiguous():
         raise ValueError("q (dense), block_tables and context_lens do not fit together")
-    out = _allocate(lambda: torch.empty_like(q), given) if out is None else _like(out, q, "out")
+    if out is not None:
+        _like(out, q, "out", dev)
+    elif stream is None:
+        out = torch.empty_like(q)
+    else:
+        out = _allocate(lambda: torch.empty_like(q), stream)
     wp, ws_bytes = None, 0
     if workspace is None:
         need = pkv_decode_scaled_workspace_bytes(cache, s, h, max_context_len, partition_size)
         if need > 0:
             workspace = _allocate(
-                lambda: torch.empty(need, dtype=torch.uint8, device=q.device), given)
+                lambda: torch.empty(need, dtype=torch.uint8, device=q.device), stream)
     if workspace is not None:
-        if not workspace.is_cuda:
-            raise ValueError("workspace must be on the GPU")
+        if workspace.get_device() != dev:
+            raise _refuse(workspace, dev, "workspace", "")
         wp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = (_lib or load()).pkv_paged_attention_decode_scaled(
-        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), s, h,
-        _i32(block_tables, "block_tables"), width, _i32(context_lens, "context_lens"),
+        ctypes.byref(cache), _scales_of(cache, scales, dev), q.data_ptr(), _code16(q, "q"), s, h,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
         max_context_len, scale, partition_size, wp, ws_bytes,
-        None if dev_err is None else dev_err.data_ptr(), out.data_ptr(), stream)
+        None if dev_err is None else _err_flag(dev_err, dev), out.data_ptr(),
+        _handle(stream, dev))
     if st:
         raise PkvError(st, "pkv_paged_attention_decode_scaled")
     return out
@@ -596,7 +636,9 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
                                        out=None, stream=None):
     """Causal attention over a scaled cache; arguments as
     pkv_paged_attention_prefill."""
-    given, stream = stream, _current_stream(q, "q", stream)
+    dev = _here(q, "q")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
     total, h, d = q.shape
     num_seqs = context_lens.numel()
     n_tables, width = block_tables.shape
@@ -604,12 +646,18 @@ def pkv_paged_attention_prefill_scaled(cache, scales, q, cu_seqlens_q, max_q_len
             not q.is_contiguous():
         raise ValueError("q (dense), cu_seqlens_q, block_tables and context_lens do not fit "
                          "together")
-    out = _allocate(lambda: torch.empty_like(q), given) if out is None else _like(out, q, "out")
+    if out is not None:
+        _like(out, q, "out", dev)
+    elif stream is None:
+        out = torch.empty_like(q)
+    else:
+        out = _allocate(lambda: torch.empty_like(q), stream)
     st = (_lib or load()).pkv_paged_attention_prefill_scaled(
-        ctypes.byref(cache), _scales_of(cache, scales), q.data_ptr(), _code16(q, "q"), num_seqs, h,
-        _i32(cu_seqlens_q, "cu_seqlens_q"), total, max_q_len, _i32(block_tables, "block_tables"),
-        width, _i32(context_lens, "context_lens"), max_context_len, scale,
-        None if dev_err is None else dev_err.data_ptr(), out.data_ptr(), stream)
+        ctypes.byref(cache), _scales_of(cache, scales, dev), q.data_ptr(), _code16(q, "q"),
+        num_seqs, h, _i32(cu_seqlens_q, "cu_seqlens_q", dev), total, max_q_len,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
+        max_context_len, scale, None if dev_err is None else _err_flag(dev_err, dev),
+        out.data_ptr(), _handle(stream, dev))
     if st:
         raise PkvError(st, "pkv_paged_attention_prefill_scaled")
     return out
@@ -629,18 +677,29 @@ def pkv_copy_blocks_scaled(caches, scales, block_pairs, dst=None, dst_scales=Non
         raise ValueError("one array of scales per layer, and as many layers on both sides")
     if block_pairs.dtype is not torch.int64 or not block_pairs.is_contiguous():
         raise ValueError("block_pairs must be contiguous int64 [n, 2]")
+    if dst is None:
+        dev = _here(block_pairs, "block_pairs")
+    else:
+        # a pool may be in pinned host memory (which the library checks), and so
+        # may the pairs; what is on a GPU is on this one
+        dev = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+        if block_pairs.is_cuda and block_pairs.get_device() != dev:
+            raise _refuse(block_pairs, dev, "block_pairs", "")
+    for c in caches if dst is None else (*caches, *dst):
+        if _elsewhere(c, dev) and (dst is None or c.device != -1):
+            raise ValueError("the cache must be on the current CUDA device")
+
+    def addresses(descs, ts):
+        return ptrs(*[_scales_of(c, t, -1 if dst is not None and not t.is_cuda else dev)
+                      for c, t in zip(descs, ts)])
+
     ptrs = ctypes.c_void_p * n
-    a = (CacheDesc * n)(*caches)
-    a_s = ptrs(*[_scales_of(c, t, dst is not None) for c, t in zip(caches, scales)])
+    a, a_s = (CacheDesc * n)(*caches), addresses(caches, scales)
     b = b_s = None
     if dst is not None:
-        b = (CacheDesc * n)(*dst)
-        b_s = ptrs(*[_scales_of(c, t, True) for c, t in zip(dst, dst_scales)])
-        stream = _stream(stream)
-    else:
-        stream = _current_stream(block_pairs, "block_pairs", stream)
+        b, b_s = (CacheDesc * n)(*dst), addresses(dst, dst_scales)
     st = (_lib or load()).pkv_copy_blocks_scaled(
         a, a_s, b, b_s, n, block_pairs.data_ptr(), block_pairs.numel() // 2,
-        None if dev_err is None else dev_err.data_ptr(), stream)
+        None if dev_err is None else _err_flag(dev_err, dev), _handle(stream, dev))
     if st:
         raise PkvError(st, "pkv_copy_blocks_scaled")

@@ -109,3 +109,86 @@ def test_calls_on_another_stream_in_a_captured_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(want, got))
     assert int(b.err.item()) == 0
+
+
+class Elsewhere:
+    """A tensor as it would look on another GPU."""
+
+    def __init__(self, t):
+        self._t = t
+
+    def get_device(self):
+        return self._t.get_device() + 1
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def arguments():
+    """name of a call -> (function, arguments that it takes without complaint)"""
+    b = Batch(310, W.F16, 4, 2, 64, 16, [1, 1], [20, 5])
+    q = b.dev16(b.q)
+    f = torch.from_numpy(freqs(64)).cuda()
+    common = dict(cache=b.desc, scales=b.gs, q=q, block_tables=b.gt, context_lens=b.gctx,
+                  max_context_len=21, dev_err=b.err)
+    attend = dict(common, scale=0.125, out=torch.empty_like(q))
+    n = B.pkv_decode_scaled_workspace_bytes(b.desc, 2, 4, 21, 16)
+    return dict(
+        rope=(B.pkv_rope_append, dict(common, k=b.dev16(b.nk), v=b.dev16(b.nv), inv_freq=f,
+                                      cu_seqlens_q=b.gcu, max_q_len=1, q_out=torch.empty_like(q))),
+        decode=(B.pkv_paged_attention_decode_scaled,
+                dict(attend, partition_size=16,
+                     workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))),
+        prefill=(B.pkv_paged_attention_prefill_scaled,
+                 dict(attend, cu_seqlens_q=b.gcu, max_q_len=1)),
+        copy=(B.pkv_copy_blocks_scaled,
+              dict(caches=b.desc, scales=b.gs, dev_err=b.err,
+                   block_pairs=torch.tensor([[0, 1]], device="cuda"))))
+
+
+def elsewhere(name, value):
+    if name not in ("cache", "caches"):
+        return Elsewhere(value)
+    c = B.CacheDesc(*(getattr(value, f) for f, _ in B.CacheDesc._fields_))
+    c.device = value.device + 1
+    return c
+
+
+@pytest.mark.parametrize("call", ["rope", "decode", "prefill", "copy"])
+@pytest.mark.parametrize("where", ["host", "gpu"])
+def test_every_tensor_has_to_be_on_the_current_device(call, where):
+    fn, good = arguments()[call]
+    fn(**good)
+    torch.cuda.synchronize()
+    for name, value in good.items():
+        if isinstance(value, torch.Tensor):
+            bad = value.cpu() if where == "host" else elsewhere(name, value)
+        elif isinstance(value, B.CacheDesc):
+            if where == "host":
+                t = torch.zeros(value.num_blocks, value.num_kv_heads, value.block_size,
+                                value.head_dim, dtype=torch.uint8)
+                bad = B.cache_desc(t, t)
+            else:
+                bad = elsewhere(name, value)
+        else:
+            continue
+        what = "the cache" if name in ("cache", "caches") else name
+        with pytest.raises(ValueError, match="%s must be on the current CUDA device" % what):
+            fn(**dict(good, **{name: bad}))
+
+
+@pytest.mark.parametrize("name", ["caches", "scales", "dst", "dst_scales", "block_pairs"])
+def test_a_pool_of_another_gpu_is_refused(name):
+    """Between two pools: host memory may take part, another GPU's not."""
+    _, good = arguments()["copy"]
+    k = torch.zeros(good["caches"].num_blocks, 2, 16, 64, dtype=torch.uint8, device="cuda")
+    good = dict(good, dst=B.cache_desc(k, k.clone()), dst_scales=torch.ones_like(good["scales"]))
+    B.pkv_copy_blocks_scaled(**good)
+    torch.cuda.synchronize()
+    bad = good[name]
+    if isinstance(bad, torch.Tensor):
+        bad = Elsewhere(bad)
+    else:
+        bad = elsewhere("cache", bad)
+    with pytest.raises(ValueError, match="must be on the current CUDA device"):
+        B.pkv_copy_blocks_scaled(**dict(good, **{name: bad}))
