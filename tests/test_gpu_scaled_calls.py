@@ -192,3 +192,59 @@ def test_a_pool_of_another_gpu_is_refused(name):
         bad = elsewhere("cache", bad)
     with pytest.raises(ValueError, match="must be on the current CUDA device"):
         B.pkv_copy_blocks_scaled(**dict(good, **{name: bad}))
+
+
+@pytest.mark.parametrize("call,name,change,error,match", [
+    ("rope", "k", lambda t: t.float(), TypeError, "k must be float16 or bfloat16"),
+    ("rope", "k", lambda t: t.bfloat16(), ValueError, "k and v must be alike"),
+    ("rope", "k", lambda t: t[:, :1], ValueError, "k and v must be alike"),
+    ("rope", "v", lambda t: t[:1], ValueError, "k and v must be alike"),
+    ("rope", "v", lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), ValueError,
+     "v must be .tokens, heads, head_dim. with dense heads"),
+    ("rope", "q", lambda t: t[:1], ValueError, "q must be alike k"),
+    ("rope", "q", lambda t: t.bfloat16(), ValueError, "q must be alike k"),
+    ("rope", "q", lambda t: t[:, :, ::2], ValueError, "q must be alike k"),
+    ("rope", "q", lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), ValueError,
+     "q must be .tokens, heads, head_dim. with dense heads"),
+    ("rope", "q_out", lambda t: t[:1], ValueError, "q_out must be dense and like q"),
+    ("rope", "q_out", lambda t: t.bfloat16(), ValueError, "q_out must be dense and like q"),
+    ("rope", "inv_freq", lambda t: t.float(), ValueError, "inv_freq must be contiguous float64"),
+    ("rope", "inv_freq", lambda t: t[::2], ValueError, "inv_freq must be contiguous float64"),
+    ("rope", "cu_seqlens_q", lambda t: t[:2], ValueError, "cu_seqlens_q needs num_seqs"),
+    ("rope", "block_tables", lambda t: t[:1], ValueError, "block_tables num_seqs rows"),
+    ("decode", "q", lambda t: t.float(), TypeError, "q must be float16 or bfloat16"),
+    ("decode", "q", lambda t: t[:1], ValueError, "do not fit together"),
+    ("decode", "q", lambda t: t[:, :, :32], ValueError, "do not fit together"),
+    ("decode", "out", lambda t: t[:, :2], ValueError, "out must be dense and like q"),
+    ("decode", "block_tables", lambda t: t[:1], ValueError, "do not fit together"),
+    ("prefill", "q", lambda t: t.float(), TypeError, "q must be float16 or bfloat16"),
+    ("prefill", "q", lambda t: t[:, :, :32], ValueError, "do not fit together"),
+    ("prefill", "out", lambda t: t.bfloat16(), ValueError, "out must be dense and like q"),
+    ("prefill", "cu_seqlens_q", lambda t: t[:2], ValueError, "do not fit together"),
+    ("copy", "block_pairs", lambda t: t.int(), ValueError, "block_pairs must be contiguous int64"),
+    ("copy", "scales", lambda t: [t, t], ValueError, "one array of scales per layer"),
+] + [(call, "scales", change, ValueError, "scales must be contiguous float32")
+     for call in ("rope", "decode", "prefill", "copy")
+     for change in (lambda t: t[:3], lambda t: t.half(), lambda t: t.double(), lambda t: t[..., :1])
+] + [(call, name, change, ValueError, "%s must be contiguous int32" % name)
+     for call in ("rope", "decode", "prefill")
+     for name in ("block_tables", "context_lens", "cu_seqlens_q")
+     if call != "decode" or name != "cu_seqlens_q"
+     for change in (lambda t: t.long(), lambda t: torch.stack([t, t], -1)[..., 0])
+] + [(call, "dev_err", lambda t: t.long(), ValueError, "dev_err must be int32")
+     for call in ("rope", "decode", "prefill", "copy")])
+def test_what_the_binding_refuses(call, name, change, error, match):
+    """One argument changed at a time: the refusal is that argument's own."""
+    fn, good = arguments()[call]
+    fn(**good)
+    torch.cuda.synchronize()
+    args = dict(good)
+    if call == "copy" and name == "scales" and match.startswith("one array"):
+        args["caches"] = [args["caches"]]
+    args[name] = change(args[name])
+    if name == "k" and match.startswith("k must"):
+        args["v"] = args["v"].float()
+    if name in ("q",) and "out" in args:
+        args["out"] = None
+    with pytest.raises(error, match=match):
+        fn(**args)
