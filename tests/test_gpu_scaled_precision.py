@@ -71,10 +71,15 @@ def bounds(b, scale, decode):
     return err
 
 
+def with_output(b, ref, err):
+    """err and the output's own rounding."""
+    return err + torch.finfo(TD[b.dt]).eps / 2 * (np.abs(ref) + err) + \
+        (2.0 ** -25 if b.dt == W.F16 else 0.0)
+
+
 def assert_within(got, b, scale, what, decode):
-    ref, err = b.attention(scale), bounds(b, scale, decode)
-    bound = err + torch.finfo(TD[b.dt]).eps / 2 * (np.abs(ref) + err)
-    bound = bound + (2.0 ** -25 if b.dt == W.F16 else 0.0)
+    ref = b.attention(scale)
+    bound = with_output(b, ref, bounds(b, scale, decode))
     off = np.abs(H.out_to_double(got) - ref)
     assert (off <= bound).all(), (what, float((off / np.maximum(bound, 1e-300)).max()), off.max())
     assert int(b.err.item()) == 0
@@ -164,3 +169,39 @@ def test_one_block_far_above_the_others(which, log2):
     assert_within(b.prefill(scale), b, scale, "prefill", False)
     b.q, b.cu = np.ascontiguousarray(b.q[-1:]), np.array([0, 1], np.int32)
     assert_within(b.decode(scale), b, scale, "decode", True)
+
+
+@pytest.mark.parametrize("partition", [0, 64, 1024])
+@pytest.mark.parametrize("heads,kv,d,bs,n,hi", [
+    (6, 2, 64, 8, 60, 1500), (16, 1, 128, 16, 3, 4000), (4, 4, 128, 32, 9, 2000),
+    (8, 1, 64, 16, 1, 5000), (2, 2, 64, 16, 300, 1100), (24, 2, 128, 8, 33, 3000)])
+def test_every_token_counts_once_wherever_shares_are_cut(heads, kv, d, bs, n, hi, partition):
+    """Equal weights, and V of token t in channel t mod D alone: a token lost or
+    counted twice changes its channel by one part in (tokens / D), several times
+    the bound.  Lengths around every multiple that matters."""
+    r = np.random.default_rng(400 + n)
+    edges = np.array([0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 191, 192, 193, 1023, 1024, 1025])
+    ctx = np.where(r.random(n) < 0.4, edges[r.integers(0, len(edges), n)], r.integers(0, hi, n))
+    ctx[-1] = hi
+    b = Batch(401, W.F16, heads, kv, d, bs, [1] * n, ctx, fill=False)
+    b.ctx = ctx.astype(np.int32)
+    b.k[...] = 0
+    b.v[...] = 0
+    b.scales[...] = 1
+    for s, c in enumerate(b.ctx):
+        t = np.arange(c)
+        phys = b.tables[s, t // bs]
+        for h in range(kv):
+            b.scales[phys, h, 1] = 2.0 ** r.integers(-3, 4)
+            b.v[phys, h, t % bs, t % d] = 0x38 + r.integers(0, 8, c)      # 1 to 15 / 8
+    b.upload()
+    if partition == 0:
+        from paged_kv_cache_130_gb300 import binding as B
+        assert B.pkv_decode_scaled_partition_size(b.desc, n, heads, hi) == 0
+    bound = with_output(b, b.attention(0.125), bounds(b, 0.125, True))
+    for s, c in enumerate(b.ctx):
+        for h in range(kv):
+            if c:
+                token = b.scales[b.tables[s, 0], h, 1] / c
+                assert token > 5 * bound[s, h * heads // kv:(h + 1) * heads // kv].max()
+    assert_within(b.decode(0.125, partition_size=partition), b, 0.125, "tokens", True)
