@@ -491,15 +491,17 @@ pkv_status pkv_paged_attention_decode_static_ws(const pkv_cache_desc* cache,
  *
  * cache, scales  scales NULL: the cache as pkv_kv_append takes it (in_dtype, or
  *                E4M3 with k_scale / v_scale).  Otherwise a scaled cache:
- *                bound = max(1, sqrt2 |mscale|) max|K| before the rotation, or
- *                max|V|, over the finite elements that the call writes into
- *                the block for that head, and need = the smallest power of two
+ *                bound = max(1, sqrt2 |mscale|) max|K| before the rotation
+ *                (max|K| when rot_dim is 0), or max|V|, over the finite
+ *                elements that the call writes into the block for that head,
+ *                and need = the smallest power of two
  *                s >= 2^-126 with bound <= 448 s.  A block whose first slot
  *                the call writes gets scale = need; any other block keeps the
  *                larger of its scale and need, and when that is larger than
  *                it was, the codes of its other slots become
- *                E4M3(code * old / new).  New codes are E4M3(x / scale), to
- *                nearest even; infinities saturate, NaN stays NaN.
+ *                E4M3(code * old / new).  New codes are
+ *                E4M3(x * (1.0f / scale)), to nearest even; infinities
+ *                saturate, NaN stays NaN.
  * q, k, v        device [total_q][num_heads or num_kv_heads][head_dim] of
  *                in_dtype; q_stride, k_stride, v_stride: elements between
  *                tokens (a multiple of 8; slices of one projection's output

@@ -205,3 +205,35 @@ def test_every_token_counts_once_wherever_shares_are_cut(heads, kv, d, bs, n, hi
                 token = b.scales[b.tables[s, 0], h, 1] / c
                 assert token > 5 * bound[s, h * heads // kv:(h + 1) * heads // kv].max()
     assert_within(b.decode(0.125, partition_size=partition), b, 0.125, "tokens", True)
+
+
+@pytest.mark.parametrize("bs", [8, 16, 32])
+def test_append_beside_a_scale_of_the_callers(bs):
+    """A part-filled block whose scale is no power of two: kept while it is large
+    enough, its codes re-rounded to the new one otherwise."""
+    import oracle
+    r = np.random.default_rng(500 + bs)
+    new = 3
+    for k_scale, v_scale in ((0.7, 0.3), (0.7, 1e-3), (1e-4, 0.0123)):
+        b = Batch(501, W.BF16, 2, 2, 64, bs, [new], [bs + 2], fill=False)
+        phys = b.tables[0, 1]
+        b.k[phys], b.v[phys] = (r.integers(0, 0x7f, b.k[phys].shape) for _ in range(2))
+        b.scales[phys, :, 0], b.scales[phys, :, 1] = k_scale, v_scale
+        b.upload()
+        b.append(None)
+        torch.cuda.synchronize()
+        for i, (codes, x) in enumerate(((b.k, b.nk), (b.v, b.nv))):
+            got = (b.gk, b.gv)[i].cpu().numpy()
+            for h in range(2):
+                old = b.scales[phys, h, i]
+                need = OS.power_of_two_scale(np.float32(np.abs(x[:, h]).max()))
+                sc = max(old, need)
+                want = codes[phys, h].copy()
+                if sc != old:
+                    want = oracle.encode_e4m3((oracle.decode(oracle.E4M3, want) *
+                                               (float(old) / float(sc))).astype(np.float32))
+                want[2:2 + new] = oracle.encode_e4m3(x[:, h].astype(np.float32) *
+                                                     (np.float32(1) / sc))
+                assert b.gs[phys, h, i].item() == sc
+                assert np.array_equal(got[phys, h], want), (k_scale, v_scale, i, h)
+        assert int(b.err.item()) == 0
