@@ -542,9 +542,9 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
  * partition_size gives the partitions, workspace layout and reduce of
  * pkv_paged_attention_decode.  pkv_decode_scaled_partition_size tells the choice
  * (0: equal shares), pkv_decode_scaled_workspace_bytes the scratch it needs.
- * A block with a bad id contributes nothing.  The same inputs and partition
- * size give the same bits on one kind of GPU.  Calls that can overlap on the GPU
- * need workspaces of their own.
+ * scale has to be finite.  A block with a bad id contributes nothing.  The same
+ * inputs and partition size give the same bits on one kind of GPU.  Calls that
+ * can overlap on the GPU need workspaces of their own.
  * Scales are positive and finite; V of a block loses no precision while its scale
  * is within 2^20 of the context's largest.
  * ------------------------------------------------------------------------- */
@@ -568,8 +568,8 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
 /* ---------------------------------------------------------------------------
  * Causal attention of prompts and chunks over a scaled cache:
  * pkv_paged_attention_prefill with k_t and v_t = code * scale of their block and
- * KV head.  q and out F16 or BF16, 1..128 query heads per KV head.  A block
- * with a bad id reads as zeros; a token that a row may not see does not reach
+ * KV head.  q and out F16 or BF16, 1..128 query heads per KV head; scale has to
+ * be finite.  A block with a bad id reads as zeros; a token that a row may not see does not reach
  * it, whatever its codes are.  Scales are positive, normal and finite, of any
  * value; powers of two, as pkv_rope_append writes them, are up to a quarter
  * faster.  Codes of a block whose scale is more than 2^22 below the largest of

@@ -250,7 +250,8 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
     if (st != PKV_OK)
         return st;
     if (!is16(q_dtype) || num_seqs < 0 || num_heads <= 0 || num_heads % cache->num_kv_heads != 0 ||
-        !lengths_ok(max_blocks_per_seq, max_context_len, cache->block_size) || partition_size < 0 ||
+        !lengths_ok(max_blocks_per_seq, max_context_len, cache->block_size) ||
+        !(fabsf(scale) < INFINITY) || partition_size < 0 ||
         partition_size % cache->block_size != 0 || partition_size % 16 != 0)
         return PKV_ERR_INVALID_ARG;
     if (num_heads / cache->num_kv_heads > 16)
@@ -332,7 +333,7 @@ pkv_status pkv_paged_attention_prefill_scaled(
     if (st != PKV_OK)
         return st;
     if (!is16(q_dtype) || num_seqs < 0 || num_heads <= 0 || num_heads % cache->num_kv_heads != 0 ||
-        total_q < 0 || max_q_len < 0 ||
+        total_q < 0 || max_q_len < 0 || !(fabsf(scale) < INFINITY) ||
         !lengths_ok(max_blocks_per_seq, max_context_len, cache->block_size))
         return PKV_ERR_INVALID_ARG;
     if (num_heads / cache->num_kv_heads > 128)

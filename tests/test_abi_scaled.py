@@ -182,3 +182,12 @@ def test_binding_checks():
         B.pkv_paged_attention_decode_scaled(d, s, q, t, c, 3, 0.1)
     with pytest.raises(ValueError):
         B.pkv_copy_blocks_scaled([d, d], [s], torch.zeros(1, 2, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attention_scale_has_to_be_finite(lib, scale):
+    """The prefill would answer a NaN with numbers."""
+    a = dict(DECODE, scale=scale)
+    assert lib.pkv_paged_attention_decode_scaled(ctypes.byref(_desc()), *a.values()) == INVALID
+    a = dict(PREFILL, scale=scale)
+    assert lib.pkv_paged_attention_prefill_scaled(ctypes.byref(_desc()), *a.values()) == INVALID
