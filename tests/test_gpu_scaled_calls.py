@@ -248,3 +248,53 @@ def test_what_the_binding_refuses(call, name, change, error, match):
         args["out"] = None
     with pytest.raises(error, match=match):
         fn(**args)
+
+
+def test_more_sequences_than_a_grid_has_rows():
+    """70,000 sequences: a prompt of one token each, appended and prefilled, and
+    decoded; each attends to itself alone, so its output is its stored V."""
+    n, kv, bs, d = 70000, 1, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(n, 4, d, generator=g, device="cuda").half()
+    q, k, v = x[:, :2], x[:, 2:3], x[:, 3:]
+    codes = [torch.full((n, kv, bs, d), 0xff, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    sc = torch.full((n, kv, 2), float("nan"), device="cuda")
+    desc = B.cache_desc(*codes)
+    tables = torch.randperm(n, generator=g, device="cuda").int()[:, None].contiguous()
+    ctx = torch.ones(n, dtype=torch.int32, device="cuda")
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qr = B.pkv_rope_append(desc, q, k, v, None, cu, 1, tables, ctx, 1, scales=sc, dev_err=err)
+    pre = B.pkv_paged_attention_prefill_scaled(desc, sc, qr, cu, 1, tables, ctx, 1, 0.125, dev_err=err)
+    dec = B.pkv_paged_attention_decode_scaled(desc, sc, qr, tables, ctx, 1, 0.125, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(qr, q)
+    ids = tables[:, 0].long()
+    stored = codes[1][ids, 0, 0].view(torch.float8_e4m3fn).double() * sc[ids, 0, 1:].double()
+    # half an E4M3 step of the value, or half a subnormal step
+    off = (stored - v[:, 0].double()).abs()
+    assert (off <= torch.maximum(2.0 ** -4 * v[:, 0].double().abs(), 2.0 ** -10 * sc[ids, 0, 1:].double())).all()
+    assert (codes[1][:, :, 1:] == 0xff).all()
+    # a single weight of 1 (over a sum of 1): the value itself, in fp16
+    for out in (pre, dec):
+        assert torch.equal(out[:, 0], stored.half()) and torch.equal(out[:, 1], stored.half())
+
+
+def test_copy_of_more_pairs_and_layers_than_one_launch_takes():
+    n, layers = 66000, 65
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randint(0, 256, (2 * n, 1, 8, 64), dtype=torch.uint8, device="cuda", generator=g)
+    v, s = k.flip(0), torch.rand(2 * n, 1, 2, device="cuda", generator=g)
+    order = torch.randperm(2 * n, device="cuda", generator=g)
+    pairs = order.view(2, n).t().contiguous()
+    B.pkv_copy_blocks_scaled(B.cache_desc(k, v), s, pairs)
+    for t in (k, v, s):
+        assert torch.equal(t[pairs[:, 1]], t[pairs[:, 0]])
+    ks = torch.randint(0, 256, (layers, 6, 1, 8, 64), dtype=torch.uint8, device="cuda", generator=g)
+    vs, ss = ks.flip(0), torch.rand(layers, 6, 1, 2, device="cuda", generator=g)
+    before = [t.clone() for t in (ks, vs, ss)]
+    B.pkv_copy_blocks_scaled([B.cache_desc(a, b) for a, b in zip(ks, vs)], list(ss),
+                             torch.tensor([[1, 4], [2, 5]], device="cuda"))
+    for t, u in zip((ks, vs, ss), before):
+        u[:, 4:] = u[:, 1:3].clone()
+        assert torch.equal(t, u)

@@ -125,6 +125,9 @@ SCALES = [
     (W.F16, 4, 2, 64, 8, [3, 130, 1], [700, 40, 0]),
     (W.BF16, 8, 1, 128, 16, [40, 300], [500, 0]),
     (W.F16, 16, 2, 128, 32, [20, 1, 17], [100, 1100, 15]),
+    (W.BF16, 6, 2, 128, 8, [129, 2], [900, 0]),
+    (W.F16, 7, 1, 64, 32, [50], [1400]),
+    (W.BF16, 2, 2, 64, 16, [300, 9], [0, 2000]),
 ]
 
 
