@@ -545,8 +545,12 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
  * scale has to be finite.  A block with a bad id contributes nothing.  The same
  * inputs and partition size give the same bits on one kind of GPU.  Calls that
  * can overlap on the GPU need workspaces of their own.
- * Scales are positive and finite; V of a block loses no precision while its scale
- * is within 2^20 of the context's largest.
+ * Scales are positive, normal and finite.  A token's weight times its block's V
+ * scale is rounded to fp16: by 2^-11 of itself at most, or by 2^-30 of the largest
+ * weight times the context's largest V scale where that is more.  Equal shares
+ * count units of 64 tokens in 31 bits: the contexts of a batch hold fewer than
+ * 2^36 tokens in all.  Few sequences of up to 1,024 tokens are faster with a
+ * partition_size of 256 than with the library's choice.
  * ------------------------------------------------------------------------- */
 int32_t pkv_decode_scaled_partition_size(const pkv_cache_desc* cache, int32_t num_seqs,
                                          int32_t num_heads, int32_t max_context_len,
@@ -569,12 +573,13 @@ pkv_status pkv_paged_attention_decode_scaled(const pkv_cache_desc* cache, const 
  * Causal attention of prompts and chunks over a scaled cache:
  * pkv_paged_attention_prefill with k_t and v_t = code * scale of their block and
  * KV head.  q and out F16 or BF16, 1..128 query heads per KV head; scale has to
- * be finite.  A block with a bad id reads as zeros; a token that a row may not see does not reach
- * it, whatever its codes are.  Scales are positive, normal and finite, of any
- * value; powers of two, as pkv_rope_append writes them, are up to a quarter
- * faster.  Codes of a block whose scale is more than 2^22 below the largest of
- * the context are off by up to 2^-31 of that scale.  Weights are rounded to fp16:
- * by 2^-11 of themselves at most, or 2^-31 of the row's largest.
+ * be finite.  A block with a bad id reads as zeros; a token that a row may not
+ * see does not reach it, whatever its codes are.  Scales are positive, normal and
+ * finite; powers of two, as pkv_rope_append writes them, are up to a quarter
+ * faster than others.  K and V of a block whose scale is more than 2^22 below the
+ * context's largest are off by up to 2^-31 of that scale.  Weights are rounded to
+ * fp16: by 2^-11 of themselves at most, or by 2^-31 of the row's largest where
+ * that is more.
  * Device checks: as for the prefill.  Launches: one kernel; a CTA holds up to 256
  * (token, query head) rows of a KV head and walks every key they see, so a few
  * tokens after a long context (drafted ones, say) are better decoded, each as a

@@ -23,9 +23,10 @@
 //     tokens 2t, 2t + 1, 2t + 8, 2t + 9 for its 1/8 of head_dim; a byte permute
 //     pairs two tokens' codes, and the conversion to fp16 yields the operand.
 //     P^T comes from the scores through movmatrix.  The weights are rounded to
-//     fp16 (11 bits, relative 2^-12 at most each) after the multiplication by
-//     vs / vref 2^6, vref = the largest vs so far: fp16 keeps that exact to
-//     ratios of 2^-20, and what it loses below is 2^-31 of vref's block.
+//     fp16 after the multiplication by vs / vref 2^6, vref = at most twice the
+//     largest vs so far: each is off by at most 2^-11 of itself, or, where that
+//     product is subnormal (a weight times vs below 2^-19 or so of the largest of
+//     both), by 2^-30 of the largest weight times the largest vs.
 // The running maximum, sums and the output accumulators are fp32.
 //
 // Bound by HBM where contexts are long: 16 of 8,192..32,768 tokens, 32 heads, D
@@ -779,6 +780,14 @@ int64_t decode_scaled_partial_rows(int32_t group, int sms)
 // 512..2048 76 / 71, of 1024..4096 137 / 120, 2,048 of 256..1024 70 / 69, of
 // 1024..4096 232 / 216, 8,192 of 256..1024 249 / 248, of 2048..8192 1633 / 1634:
 // the shares' second launch and walk against the imbalance of the last wave.
+// Few items of exactly 256, 512, 768, 1,024 tokens, 8 heads each, D = 128:
+//   1 item    6.7 /  8.5   9.3 / 11.3  11.8 / 12.4  14.1 / 11.9
+//   8 items   6.5 / 13.0   9.1 / 12.9  11.6 / 13.6  13.9 / 13.4
+//   32 items  6.7 / 13.5  10.5 / 14.1  13.8 / 14.7  17.0 / 15.1
+// and D = 64: 1 item 5.5 / 7.2, 7.5 / 9.6, 9.4 / 10.7, 11.2 / 10.3; 32 items 5.6 /
+// 11.4, 7.7 / 11.5, 9.8 / 12.0, 13.6 / 12.9.  One pass loses up to a sixth at its
+// very end.  Explicit partitions of 256 tokens beat both there (D = 128: 7.7,
+// 7.8 and 7.8 us for 1 item of 512, 768, 1,024; 32 items 8.4, 8.8 and 9.0).
 int32_t decode_scaled_partition(const DecodeParams& p)
 {
     const int32_t bs = p.block_size < 16 ? 16 : p.block_size;

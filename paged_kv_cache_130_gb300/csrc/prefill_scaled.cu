@@ -14,13 +14,13 @@
 //     The scale's power of two goes into the conversion: a block's K becomes
 //     code * 2^(e - eref + 7) with 2^eref the power of two of the CTA's largest
 //     ks (V alike), which fp16 holds exactly down to 2^-22 of the largest; what
-//     a block further down loses is at most 2^-32 of the largest scale.  So one
+//     a block further down loses is at most 2^-31 of the largest scale.  So one
 //     factor serves all scores, one all outputs, and while the scales are powers
 //     of two, as the append makes them, the softmax does not know about blocks.
 //     Otherwise the rest of each scale, in [1, 2), multiplies its block's scores
 //     and weights there, in fp32 (rounding it into the fp16 factor moved all
-//     scores of a block by up to 2^-11); chunks then take 281 us instead of 227,
-//     prompts 198 instead of 175.
+//     scores of a block by up to 2^-11); chunks then take 281 us instead of 226,
+//     prompts 198 instead of 174.
 //   * warps 8 and 10 (one issuing thread each): O_w += P_w(j-1) V(j-1), then
 //     S_w(j) = Q_w K(j)^T, taking turns by slot.
 //   * warps 0-3 and 4-7: softmax, one thread per row.  q is fp16 per row times
@@ -38,8 +38,9 @@
 // Bound by the chain of a slot (scores, softmax, product: ~3,500 cycles for 32
 // products of 128 x 128 x 16, of which the tensor core is busy ~2,700), and by
 // ~8,000 cycles to a CTA's first product. Measured: 4 chunks of 512 tokens after
-// 1,024..4,096 (64 heads over 8, D 128, block 16) 222 us, 1,025 TFLOP/s; 8 prompts
-// of 512..2,048 tokens (32 heads) 172 us, 575 TFLOP/s. Beside it, the chunks:
+// 1,024..4,096 (64 heads over 8, D 128, block 16) 226 us, 1,010 TFLOP/s; 8 prompts
+// of 512..2,048 tokens (32 heads) 174 us, 568 TFLOP/s. (Scales of any value cost
+// 1.3 % of that: 223 and 172 us without.) Beside it, on the way, the chunks:
 // codes waited for as they are read 391 us, kept in registers 263-313, conversion
 // two vectors at a time 255, weights handed over whole 259, on the half 246.
 #include <cuda.h>

@@ -11,7 +11,10 @@ the frequencies handed to it.  The kinds here:
 * yarn: by parts (Peng et al., "YaRN", 2023): pairs that turn more than
   ``beta_fast`` times over the trained length stay, pairs that turn less than
   ``beta_slow`` times are divided by ``factor``, linear in the turns between;
-  q and K are multiplied by ``0.1 ln(factor) + 1``.
+  q and K are multiplied by ``0.1 ln(factor) + 1``.  This is the paper's ramp.
+  Implementations that ramp linearly over the pair's index instead give other
+  frequencies in between: for a checkpoint trained with those, hand its own
+  frequencies to the call.
 """
 import math
 
