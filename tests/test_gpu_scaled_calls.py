@@ -298,3 +298,54 @@ def test_copy_of_more_pairs_and_layers_than_one_launch_takes():
     for t, u in zip((ks, vs, ss), before):
         u[:, 4:] = u[:, 1:3].clone()
         assert torch.equal(t, u)
+
+
+@pytest.mark.parametrize("kv,heads,d,bs,cached,partition", [
+    (8, 8, 64, 16, 20, 0), (8, 64, 128, 16, 1300, 0), (32, 32, 128, 32, 40, 0), (4, 16, 64, 32, 600, 64)])
+def test_decode_right_behind_an_append_that_raises_scales(kv, heads, d, bs, cached, partition):
+    """The decode starts while the append before it ends: it has to see the raised
+    scales and re-rounded codes that other SMs wrote.  Every new token is twice the
+    one before, so every append but a block's first rewrites whole blocks."""
+    n, steps = 48, 40
+    g = torch.Generator(device="cuda").manual_seed(kv)
+    width = -(-(cached + steps) // bs)
+    nb = n * width
+    codes = [torch.randint(0, 0x60, (nb, kv, bs, d), dtype=torch.uint8, device="cuda", generator=g)
+             for _ in range(2)]
+    sc = torch.full((nb, kv, 2), 2.0 ** -12, device="cuda")
+    desc = B.cache_desc(*codes)
+    tables = torch.randperm(nb, device="cuda", generator=g).int().view(n, width).contiguous()
+    f = torch.from_numpy(freqs(d)).cuda()
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    ctx = torch.empty(n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(1, B.pkv_decode_scaled_workspace_bytes(desc, n, heads, cached + steps, partition)),
+                     dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.randn(n, heads + 2 * kv, d, device="cuda", generator=g)
+    qkv = x.bfloat16()
+    out = torch.empty(n, heads, d, dtype=torch.bfloat16, device="cuda")
+    args = (tables, ctx, cached + steps, d ** -0.5, partition)
+
+    def step():
+        qr = B.pkv_rope_append(desc, qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:], f,
+                               cu, 1, tables, ctx, cached + steps, scales=sc, dev_err=err)
+        B.pkv_paged_attention_decode_scaled(desc, sc, qr, *args, workspace=ws, out=out)
+        return qr
+
+    ctx.fill_(cached + 1)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qr = step()
+    for i in range(steps):
+        ctx.fill_(cached + i + 1)
+        qkv[:, heads:] = (x[:, heads:] * 2.0 ** (i % bs - 8)).bfloat16()
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()                              # the two launches side by side
+        torch.cuda.synchronize()
+        again = B.pkv_paged_attention_decode_scaled(desc, sc, qr, *args, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)), i
+    assert int(err.item()) == 0 and not out.isnan().any()
