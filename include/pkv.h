@@ -532,6 +532,22 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
                            pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * pkv_rope_append where a token's position is not its place in the context, as
+ * after pkv_evict: row j of sequence s is rotated by position p +
+ * position_offsets[s] (device int32 [num_seqs]; NULL: 0), and stored at p.
+ * Positions lie within int32.
+ * ------------------------------------------------------------------------- */
+pkv_status pkv_rope_append_at(const pkv_cache_desc* cache, float* scales, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, int32_t in_dtype, int32_t num_heads,
+                              const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                              float mscale, int32_t num_seqs, const int32_t* cu_seqlens_q,
+                              int32_t total_q, int32_t max_q_len, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, const int32_t* context_lens,
+                              int32_t max_context_len, const int32_t* position_offsets,
+                              int32_t* dev_err, void* q_out, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Decode attention over a scaled cache: pkv_paged_attention_decode with k_t and
  * v_t = code * scale of their block and KV head.  q and out F16 or BF16, 1..16
  * query heads per KV head; partition_size a multiple of block_size and of 16,
@@ -611,6 +627,148 @@ pkv_status pkv_copy_blocks_scaled(const pkv_cache_desc* src, float* const* src_s
                                   const pkv_cache_desc* dst, float* const* dst_scales,
                                   int32_t num_layers, const int64_t* block_pairs,
                                   int64_t num_pairs, int32_t* dev_err, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Shared-prefix decode over a scaled cache: the attention of
+ * pkv_paged_attention_decode_scaled for groups of sequences that share their
+ * leading blocks, with the groups, bounds and device checks of
+ * pkv_paged_attention_decode_shared_prefix.  Sequences are groups' members in
+ * order; a shared block is read once for every 8 or 16 rows (members x query heads
+ * of a KV head) of its group.  Groups without a prefix (0 blocks) and num_groups or
+ * max_prefix_blocks of 0 give the plain decode.
+ * Members beyond max_group_size, and members of a group whose entry cannot be
+ * used, get zeros.  num_seqs + num_groups is 2,048 at most (else
+ * PKV_ERR_UNSUPPORTED).  The same inputs give the same bits on one kind of GPU.
+ * Calls that can overlap on the GPU need workspaces of their own.
+ * Launches: two kernels.
+ * ------------------------------------------------------------------------- */
+size_t pkv_decode_scaled_shared_prefix_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                                       int32_t num_heads, int32_t num_groups,
+                                                       int32_t max_group_size,
+                                                       int32_t max_context_len);
+
+pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
+    const pkv_cache_desc* cache, const float* scales, const void* q, int32_t q_dtype,
+    int32_t num_seqs, int32_t num_heads, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, int32_t max_context_len, int32_t num_groups,
+    const int32_t* group_begin, const int32_t* group_prefix_blocks, int32_t max_group_size,
+    int32_t max_prefix_blocks, float scale, void* workspace, size_t workspace_bytes,
+    int32_t* dev_err, void* out, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention weights and eviction (the pages speak of blocks being freed when a
+ * sequence ends; freeing tokens that nobody attends to is this library's).  Every
+ * sequence and KV head has a row of float totals, entry t for token t of its
+ * context:
+ *   weights  device float, entry (s, g, t) at s * weights_seq + g * weights_head + t
+ *            (strides in elements; rows hold max_context_len entries at least and do
+ *            not overlap).
+ * pkv_attention_weights adds the weights of a prompt's last rows (or of all),
+ * pkv_paged_attention_decode_scaled_weights those of a decode step; both add to
+ * what is there, so a new sequence's row starts at zero.  pkv_evict keeps the
+ * tokens of largest total; pkv_rope_append_at goes on from there.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * Attention weights of each sequence's last rows, without the attention itself.
+ * With the batch layout of the prefill, m_s = min(window, n_s) and rows j < m_s the
+ * last of sequence s, at positions p = c - m_s + j:
+ *   x_jh(t) = scale * dot(q[j][h], k_t),  t <= p
+ *   weights[s][g][t] += sum_j sum_{h of g} exp(x_jh(t) - max x_jh) / sum_t exp(x_jh(t) - max x_jh)
+ * over the query heads h of KV head g, fp32 throughout.  For a decode step n_s = 1
+ * and window 1.
+ *
+ * cache, scales  scales NULL: a 16-bit cache with q of the same type, or an E4M3
+ *                cache with k_scale; otherwise a scaled cache, whose scales are
+ *                positive, normal and finite.  V is not read.
+ * q              device [total_q][num_heads][head_dim], F16 or BF16, 1..128 query
+ *                heads per KV head (a cache of E4M3 codes takes bf16 rows as fp16
+ *                times a power of two: elements below 2^-28 of the row's largest
+ *                may be rounded).
+ * workspace      pkv_attention_weights_workspace_bytes bytes, 256-byte aligned.
+ * Device checks as for the prefill: a sequence that cannot be used gets nothing
+ * added; a key of a block with a bad id is read as zeros.  The same inputs give
+ * the same bits on one kind of GPU.
+ * Launches: three kernels.  K is read twice, and again for every further 256
+ * (row, query head) rows of a KV head.
+ * ------------------------------------------------------------------------- */
+size_t pkv_attention_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                             int32_t num_heads, int32_t window,
+                                             int32_t max_context_len);
+
+pkv_status pkv_attention_weights(const pkv_cache_desc* cache, const float* scales, const void* q,
+                                 int32_t q_dtype, int32_t num_seqs, int32_t num_heads,
+                                 const int32_t* cu_seqlens_q, int32_t total_q, int32_t window,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, int32_t max_context_len, float scale,
+                                 float* weights, int64_t weights_seq, int64_t weights_head,
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                 pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_attention_decode_scaled that adds each token's weight, summed over the
+ * query heads of its KV head, to its total, as pkv_attention_weights does.  A block
+ * with a bad id contributes nothing and gets nothing.
+ * workspace   pkv_decode_scaled_weights_workspace_bytes bytes, 256-byte aligned (it
+ *             holds every score: 4 bytes a token and query head, the latter to the
+ *             next power of two, of up to 1,024 sequences of max_context_len).
+ * Launches: one kernel for contexts up to 1,024 tokens, two beyond, for every
+ * 1,024 sequences.
+ * ------------------------------------------------------------------------- */
+size_t pkv_decode_scaled_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                                 int32_t num_heads, int32_t max_context_len);
+
+pkv_status pkv_paged_attention_decode_scaled_weights(
+    const pkv_cache_desc* cache, const float* scales, const void* q, int32_t q_dtype,
+    int32_t num_seqs, int32_t num_heads, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, int32_t max_context_len, float scale, float* weights,
+    int64_t weights_seq, int64_t weights_head, void* workspace, size_t workspace_bytes,
+    int32_t* dev_err, void* out, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Eviction -- every KV head of a sequence keeps the tokens of largest total, in
+ * blocks of their own; the caller frees the old ones.
+ *
+ * Of c = context_lens[s] tokens n = min(c, keep_lens[s]) stay, for each KV head by
+ * itself: the last l = min(keep_last, n), the first f = min(keep_first, n - l), and of
+ * those between the n - f - l of largest weight, the lower index first where weights
+ * are equal (NaN counts as -infinity).  They keep their order: kept token i goes to
+ * slot i of the new context, block dst_tables[s][i / block_size].  K stays rotated
+ * as it was: see pkv_rope_append_at.
+ *
+ * cache, scales  any cache; with scales a scaled one: the scale of a destination
+ *                block and KV head (K and V each) becomes the largest of the blocks
+ *                its tokens come from, and codes E4M3(code * (old / new)).  Slots of
+ *                the last block behind token n - 1 keep their bytes.
+ * keep_lens      device int32 [num_seqs], 0..max_keep_len.
+ * dst_tables     device int32 [num_seqs][max_dst_blocks], max_dst_blocks at least
+ *                ceil(min(max_keep_len, max_context_len) / block_size); the first
+ *                ceil(n / block_size) entries of a row are used.
+ * weights_out    rows of weights_out_len entries (at least min(max_keep_len,
+ *                max_context_len)): the totals of what stays, zeros behind.  Not
+ *                overlapping `weights`.
+ * lens_out       device int32 [num_seqs]: n.
+ * workspace      pkv_evict_workspace_bytes bytes, 256-byte aligned.
+ * Precondition (not checked): the destination blocks are distinct, and none is a
+ * block of a sequence of the batch.
+ * Device checks: a context length below 0, above max_context_len or the table, or a
+ * keep_lens entry out of range -> PKV_DEVERR_CONTEXT, lens_out 0, nothing else of that
+ * sequence is written; a bad block id -> PKV_DEVERR_BLOCK_ID, what it holds or would
+ * hold is skipped.
+ * Launches: two kernels.
+ * ------------------------------------------------------------------------- */
+size_t pkv_evict_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs, int32_t max_keep_len,
+                                 int32_t max_context_len);
+
+pkv_status pkv_evict(const pkv_cache_desc* cache, float* scales, int32_t num_seqs,
+                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                     const int32_t* context_lens, int32_t max_context_len, const float* weights,
+                     int64_t weights_seq, int64_t weights_head, const int32_t* keep_lens,
+                     int32_t max_keep_len, int32_t keep_first, int32_t keep_last,
+                     const int32_t* dst_tables, int32_t max_dst_blocks, float* weights_out,
+                     int64_t weights_out_seq, int64_t weights_out_head, int32_t weights_out_len,
+                     int32_t* lens_out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                     pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * pkv_testing_set_decode_wait_limit -- a testing aid, not part of the method

@@ -14,4 +14,8 @@ from .binding import (  # noqa: F401
     pkv_swap_blocks, pkv_copy_blocks_scaled, pkv_decode_scaled_partition_size,
     pkv_decode_scaled_workspace_bytes, pkv_paged_attention_decode_scaled,
     pkv_paged_attention_prefill_scaled, pkv_rope_append,
+    pkv_attention_weights, pkv_attention_weights_workspace_bytes,
+    pkv_decode_scaled_shared_prefix_workspace_bytes, pkv_decode_scaled_weights_workspace_bytes,
+    pkv_evict, pkv_evict_workspace_bytes, pkv_paged_attention_decode_scaled_shared_prefix,
+    pkv_paged_attention_decode_scaled_weights,
 )

@@ -93,6 +93,23 @@ def load():
                                                      i32, vp, i32, f32, vp, vp, vp]),
         "pkv_copy_blocks_scaled": (i32, [dp, ctypes.POINTER(vp), dp, ctypes.POINTER(vp), i32, vp,
                                          i64, vp, vp]),
+        "pkv_rope_append_at": (i32, [dp, vp, vp, i64, vp, i64, vp, i64, i32, i32, vp, i32, i32,
+                                     f32, i32, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp]),
+        "pkv_decode_scaled_shared_prefix_workspace_bytes": (ctypes.c_size_t, [dp, i32, i32, i32,
+                                                                              i32, i32]),
+        "pkv_paged_attention_decode_scaled_shared_prefix": (i32, [
+            dp, vp, vp, i32, i32, i32, vp, i32, vp, i32, i32, vp, vp, i32, i32, f32, vp,
+            ctypes.c_size_t, vp, vp, vp]),
+        "pkv_attention_weights_workspace_bytes": (ctypes.c_size_t, [dp, i32, i32, i32, i32]),
+        "pkv_attention_weights": (i32, [dp, vp, vp, i32, i32, i32, vp, i32, i32, vp, i32, vp, i32,
+                                        f32, vp, i64, i64, vp, ctypes.c_size_t, vp, vp]),
+        "pkv_decode_scaled_weights_workspace_bytes": (ctypes.c_size_t, [dp, i32, i32, i32]),
+        "pkv_paged_attention_decode_scaled_weights": (i32, [
+            dp, vp, vp, i32, i32, i32, vp, i32, vp, i32, f32, vp, i64, i64, vp, ctypes.c_size_t,
+            vp, vp, vp]),
+        "pkv_evict_workspace_bytes": (ctypes.c_size_t, [dp, i32, i32, i32]),
+        "pkv_evict": (i32, [dp, vp, i32, vp, i32, vp, i32, vp, i64, i64, vp, i32, i32, i32, vp,
+                            i32, vp, i64, i64, i32, vp, vp, ctypes.c_size_t, vp, vp]),
         "pkv_testing_set_decode_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),
         "pkv_testing_set_shared_prefix_path": (i32, [i32]),
         "pkv_testing_stream_copy": (i32, [vp, vp, i64, vp]),
@@ -530,11 +547,13 @@ def _like(t, ref, name, dev):
 
 def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tables, context_lens,
                     max_context_len, interleaved=False, mscale=1.0, scales=None, dev_err=None,
-                    q_out=None, stream=None):
+                    q_out=None, stream=None, position_offsets=None):
     """Rotate q and K by their positions and append K and V; returns the rotated
     q (None without q).  `inv_freq` is a float64 device tensor of rot_dim / 2
     radians per position (rope.inv_freq computes it), or None to rotate
-    nothing; with `scales` the cache is a scaled one."""
+    nothing; with `scales` the cache is a scaled one.  `position_offsets` (int32
+    [num_seqs]): how far positions are ahead of places in the context, as after
+    an eviction (pkv_rope_append_at)."""
     dev = _here(k, "k")
     if _elsewhere(cache, dev):
         raise ValueError("the cache must be on the current CUDA device")
@@ -569,13 +588,18 @@ def pkv_rope_append(cache, q, k, v, inv_freq, cu_seqlens_q, max_q_len, block_tab
     n_tables, width = block_tables.shape
     if cu_seqlens_q.numel() != num_seqs + 1 or n_tables != num_seqs:
         raise ValueError("cu_seqlens_q needs num_seqs + 1 entries, block_tables num_seqs rows")
-    st = (_lib or load()).pkv_rope_append(
+    offsets = None
+    if position_offsets is not None:
+        offsets = _i32(position_offsets, "position_offsets", dev)
+        if position_offsets.numel() != num_seqs:
+            raise ValueError("position_offsets needs num_seqs entries")
+    st = (_lib or load()).pkv_rope_append_at(
         ctypes.byref(cache), None if scales is None else _scales_of(cache, scales, dev), qp, qs,
         k.data_ptr(), _token_rows(k, "k", rows, kv, d), v.data_ptr(),
         _token_rows(v, "v", rows, kv, d), code, heads, fp, rot, interleaved, mscale, num_seqs,
         _i32(cu_seqlens_q, "cu_seqlens_q", dev), rows, max_q_len,
         _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
-        max_context_len, None if dev_err is None else _err_flag(dev_err, dev), qo,
+        max_context_len, offsets, None if dev_err is None else _err_flag(dev_err, dev), qo,
         _handle(stream, dev))
     if st:
         raise PkvError(st, "pkv_rope_append")
@@ -703,3 +727,198 @@ def pkv_copy_blocks_scaled(caches, scales, block_pairs, dst=None, dst_scales=Non
         None if dev_err is None else _err_flag(dev_err, dev), _handle(stream, dev))
     if st:
         raise PkvError(st, "pkv_copy_blocks_scaled")
+
+
+# ------------------------------------------------------------------ long contexts
+#
+# Shared prefixes over the scaled cache, attention weights, eviction.
+
+def _workspace(workspace, need, dev, stream, device):
+    """The caller's scratch, or `need` bytes: (tensor, address, bytes)."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if stream is None else \
+            _allocate(lambda: torch.empty(need, dtype=torch.uint8, device=device), stream)
+    elif workspace.get_device() != dev:
+        raise _refuse(workspace, dev, "workspace", "")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _out_like(out, q, dev, stream):
+    if out is not None:
+        return _like(out, q, "out", dev)
+    return torch.empty_like(q) if stream is None else _allocate(lambda: torch.empty_like(q), stream)
+
+
+def _totals(t, name, num_seqs, kv_heads, least, dev):
+    """Address and strides of a [num_seqs, kv_heads, >= least] float32 tensor of
+    dense rows."""
+    if t.dtype is not _F32 or t.dim() != 3 or t.get_device() != dev or t.stride(2) != 1 and \
+            t.shape[2] > 1:
+        raise _refuse(t, dev, name, "float32 [num_seqs, num_kv_heads, tokens] with dense rows")
+    n, h, w = t.shape
+    if n != num_seqs or h != kv_heads or w < least:
+        raise ValueError("%s must be [num_seqs, num_kv_heads, at least %d]" % (name, least))
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def pkv_decode_scaled_shared_prefix_workspace_bytes(cache, num_seqs, num_heads, num_groups,
+                                                    max_group_size, max_context_len):
+    return int(load().pkv_decode_scaled_shared_prefix_workspace_bytes(
+        ctypes.byref(cache), num_seqs, num_heads, num_groups, max_group_size, max_context_len))
+
+
+def pkv_paged_attention_decode_scaled_shared_prefix(cache, scales, q, block_tables, context_lens,
+                                                    max_context_len, group_begin,
+                                                    group_prefix_blocks, max_group_size,
+                                                    max_prefix_blocks, scale, workspace=None,
+                                                    dev_err=None, out=None, stream=None):
+    """Decode over a scaled cache where the sequences [group_begin[i],
+    group_begin[i+1]) share their first group_prefix_blocks[i] blocks; arguments
+    as pkv_paged_attention_decode_shared_prefix."""
+    dev = _here(q, "q")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
+    s, h, d = q.shape
+    n_tables, width = block_tables.shape
+    groups = group_prefix_blocks.numel()
+    if d != cache.head_dim or context_lens.numel() != s or n_tables != s or not q.is_contiguous():
+        raise ValueError("q (dense), block_tables and context_lens do not fit together")
+    if group_begin.numel() != groups + 1:
+        raise ValueError("group_begin needs num_groups + 1 entries")
+    code = _code16(q, "q")
+    out = _out_like(out, q, dev, stream)
+    need = 0 if workspace is not None else pkv_decode_scaled_shared_prefix_workspace_bytes(
+        cache, s, h, groups, max_group_size, max_context_len)
+    workspace, wp, ws_bytes = _workspace(workspace, need, dev, stream, q.device)
+    st = (_lib or load()).pkv_paged_attention_decode_scaled_shared_prefix(
+        ctypes.byref(cache), _scales_of(cache, scales, dev), q.data_ptr(), code, s, h,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
+        max_context_len, groups, _i32(group_begin, "group_begin", dev),
+        _i32(group_prefix_blocks, "group_prefix_blocks", dev), max_group_size, max_prefix_blocks,
+        scale, wp, ws_bytes, None if dev_err is None else _err_flag(dev_err, dev), out.data_ptr(),
+        _handle(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_attention_decode_scaled_shared_prefix")
+    return out
+
+
+def pkv_attention_weights_workspace_bytes(cache, num_seqs, num_heads, window, max_context_len):
+    return int(load().pkv_attention_weights_workspace_bytes(ctypes.byref(cache), num_seqs,
+                                                            num_heads, window, max_context_len))
+
+
+def pkv_attention_weights(cache, q, cu_seqlens_q, window, block_tables, context_lens,
+                          max_context_len, scale, weights, scales=None, workspace=None,
+                          dev_err=None, stream=None):
+    """Add the attention weights of each sequence's last `window` rows of q, summed
+    over rows and the query heads of a KV head, to `weights` (float32 [num_seqs,
+    num_kv_heads, at least max_context_len]); returns `weights`.  Any cache: with
+    `scales` a scaled one."""
+    dev = _here(q, "q")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
+    total, h, d = q.shape
+    num_seqs = context_lens.numel()
+    n_tables, width = block_tables.shape
+    if d != cache.head_dim or cu_seqlens_q.numel() != num_seqs + 1 or n_tables != num_seqs or \
+            not q.is_contiguous():
+        raise ValueError("q (dense), cu_seqlens_q, block_tables and context_lens do not fit "
+                         "together")
+    code = _code16(q, "q")
+    at, seq, head = _totals(weights, "weights", num_seqs, cache.num_kv_heads, max_context_len, dev)
+    need = 0 if workspace is not None else pkv_attention_weights_workspace_bytes(
+        cache, num_seqs, h, window, max_context_len)
+    workspace, wp, ws_bytes = _workspace(workspace, need, dev, stream, q.device)
+    st = (_lib or load()).pkv_attention_weights(
+        ctypes.byref(cache), None if scales is None else _scales_of(cache, scales, dev),
+        q.data_ptr(), code, num_seqs, h, _i32(cu_seqlens_q, "cu_seqlens_q", dev), total, window,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
+        max_context_len, scale, at, seq, head, wp, ws_bytes,
+        None if dev_err is None else _err_flag(dev_err, dev), _handle(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_attention_weights")
+    return weights
+
+
+def pkv_decode_scaled_weights_workspace_bytes(cache, num_seqs, num_heads, max_context_len):
+    return int(load().pkv_decode_scaled_weights_workspace_bytes(ctypes.byref(cache), num_seqs,
+                                                                num_heads, max_context_len))
+
+
+def pkv_paged_attention_decode_scaled_weights(cache, scales, q, block_tables, context_lens,
+                                              max_context_len, scale, weights, workspace=None,
+                                              dev_err=None, out=None, stream=None):
+    """Decode over a scaled cache that adds each token's weight, summed over the
+    query heads of its KV head, to `weights`; returns the attention's output."""
+    dev = _here(q, "q")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
+    s, h, d = q.shape
+    n_tables, width = block_tables.shape
+    if d != cache.head_dim or context_lens.numel() != s or n_tables != s or not q.is_contiguous():
+        raise ValueError("q (dense), block_tables and context_lens do not fit together")
+    code = _code16(q, "q")
+    at, seq, head = _totals(weights, "weights", s, cache.num_kv_heads, max_context_len, dev)
+    out = _out_like(out, q, dev, stream)
+    need = 0 if workspace is not None else pkv_decode_scaled_weights_workspace_bytes(
+        cache, s, h, max_context_len)
+    workspace, wp, ws_bytes = _workspace(workspace, need, dev, stream, q.device)
+    st = (_lib or load()).pkv_paged_attention_decode_scaled_weights(
+        ctypes.byref(cache), _scales_of(cache, scales, dev), q.data_ptr(), code, s, h,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
+        max_context_len, scale, at, seq, head, wp, ws_bytes,
+        None if dev_err is None else _err_flag(dev_err, dev), out.data_ptr(), _handle(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_paged_attention_decode_scaled_weights")
+    return out
+
+
+def pkv_evict_workspace_bytes(cache, num_seqs, max_keep_len, max_context_len):
+    return int(load().pkv_evict_workspace_bytes(ctypes.byref(cache), num_seqs, max_keep_len,
+                                                max_context_len))
+
+
+def pkv_evict(cache, block_tables, context_lens, max_context_len, weights, keep_lens, max_keep_len,
+              keep_first, keep_last, dst_tables, scales=None, weights_out=None, lens_out=None,
+              workspace=None, dev_err=None, stream=None):
+    """Keep, for every KV head, the tokens of largest weight: at most keep_lens[s]
+    of a context, its first and last ones among them, in the blocks of
+    `dst_tables`.  Returns (new lengths, their weights, of the shape of `weights`
+    unless `weights_out` is given)."""
+    dev = _here(context_lens, "context_lens")
+    if _elsewhere(cache, dev):
+        raise ValueError("the cache must be on the current CUDA device")
+    num_seqs = context_lens.numel()
+    n_tables, width = block_tables.shape
+    n_dst, dst_width = dst_tables.shape
+    if n_tables != num_seqs or n_dst != num_seqs or keep_lens.numel() != num_seqs:
+        raise ValueError("block_tables, dst_tables, keep_lens and context_lens do not fit together")
+    kv = cache.num_kv_heads
+    most = min(max_keep_len, max_context_len)
+    at, seq, head = _totals(weights, "weights", num_seqs, kv, max_context_len, dev)
+
+    def make(fn):
+        return fn() if stream is None else _allocate(fn, stream)
+
+    if weights_out is None:
+        weights_out = make(lambda: torch.empty(weights.shape, dtype=_F32, device=weights.device))
+    to, to_seq, to_head = _totals(weights_out, "weights_out", num_seqs, kv, most, dev)
+    if lens_out is None:
+        lens_out = make(lambda: torch.empty(num_seqs, dtype=_I32, device=weights.device))
+    elif lens_out.numel() != num_seqs:
+        raise ValueError("lens_out needs num_seqs entries")
+    need = 0 if workspace is not None else pkv_evict_workspace_bytes(cache, num_seqs, max_keep_len,
+                                                                     max_context_len)
+    workspace, wp, ws_bytes = _workspace(workspace, need, dev, stream, weights.device)
+    st = (_lib or load()).pkv_evict(
+        ctypes.byref(cache), None if scales is None else _scales_of(cache, scales, dev), num_seqs,
+        _i32(block_tables, "block_tables", dev), width, _i32(context_lens, "context_lens", dev),
+        max_context_len, at, seq, head, _i32(keep_lens, "keep_lens", dev), max_keep_len, keep_first,
+        keep_last, _i32(dst_tables, "dst_tables", dev), dst_width, to, to_seq, to_head,
+        weights_out.shape[2], _i32(lens_out, "lens_out", dev), wp, ws_bytes,
+        None if dev_err is None else _err_flag(dev_err, dev), _handle(stream, dev))
+    if st:
+        raise PkvError(st, "pkv_evict")
+    return lens_out, weights_out

@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int hchunks = p.q != nullptr ? (p.num_heads + kHeadsPerTask - 1) / kHeadsPerTask : 0;
     const int tasks = kv_tasks + T * hchunks;
 
+    const int shift = p.position_offsets != nullptr ? __ldg(p.position_offsets + s) : 0;
     // cosines and sines of the block's tokens
     for (int f = lane; f < rh; f += 32) {
         const uint64_t turns = turns_of(__ldg(p.inv_freq + f), p.per_radian);
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         float* at = sh_cs + (inter ? f : ((f >> 2) & 1) * (rh >> 1) + (f >> 3) * 4 + (f & 3));
         for (int t = warp; t < T; t += kWarps) {
             float sn, cn;
-            sincospif(half_turns(turns, lo + t), &sn, &cn);
+            sincospif(half_turns(turns, lo + t + shift), &sn, &cn);
             at[t * 2 * rh] = cn * p.mscale;
             at[t * 2 * rh + rh] = sn * p.mscale;
         }

@@ -9,68 +9,13 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <atomic>
-
+#include "api_common.h"
 #include "pkv.h"
 #include "scaled_internal.h"
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-bool is16(int32_t dt) { return dt == PKV_F16 || dt == PKV_BF16; }
-
-pkv_status from_cuda(cudaError_t e)
-{
-    if (e == cudaSuccess)
-        return PKV_OK;
-    return e == cudaErrorNotSupported ? PKV_ERR_UNSUPPORTED : PKV_ERR_CUDA;
-}
-
-// A cache descriptor; with `scaled` an E4M3 cache whose k_scale / v_scale are
-// not used.
-pkv_status check_cache(const pkv_cache_desc* c, bool scaled)
-{
-    if (c == nullptr || c->k_cache == nullptr || c->v_cache == nullptr ||
-        !aligned(c->k_cache, 16) || !aligned(c->v_cache, 16))
-        return PKV_ERR_INVALID_ARG;
-    if (c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->block_size <= 0 || c->head_dim <= 0)
-        return PKV_ERR_INVALID_ARG;
-    if (!is16(c->cache_dtype) && c->cache_dtype != PKV_FP8_E4M3)
-        return PKV_ERR_INVALID_ARG;
-    if ((c->head_dim != 64 && c->head_dim != 128) ||
-        (c->block_size != 8 && c->block_size != 16 && c->block_size != 32))
-        return PKV_ERR_UNSUPPORTED;
-    if (scaled)
-        return c->cache_dtype == PKV_FP8_E4M3 ? PKV_OK : PKV_ERR_UNSUPPORTED;
-    if (c->cache_dtype == PKV_FP8_E4M3 && (!(c->k_scale > 0.f) || !(c->v_scale > 0.f)))
-        return PKV_ERR_INVALID_ARG;
-    return PKV_OK;
-}
-
-// Sizes whose token arithmetic stays inside 32 bits.
-bool lengths_ok(int32_t max_blocks_per_seq, int32_t max_context_len, int32_t block_size)
-{
-    return max_blocks_per_seq >= 0 && max_blocks_per_seq <= INT_MAX / block_size &&
-           max_context_len >= 0 && max_context_len <= INT_MAX - 1024;
-}
-
-int device_sms()
-{
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-        return 152;
-    int v = cache[dev].load(std::memory_order_relaxed);
-    if (v <= 0) {
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-            return 152;
-        cache[dev].store(v, std::memory_order_relaxed);
-    }
-    return v;
-}
+using namespace pkv::api;
 
 struct Layout {
     int64_t parts, l_off, o_off, bytes;
@@ -137,15 +82,15 @@ void* device_address(const void* p)
 
 extern "C" {
 
-pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const void* q,
-                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                           int64_t v_stride, int32_t in_dtype, int32_t num_heads,
-                           const double* inv_freq, int32_t rot_dim, int32_t interleaved,
-                           float mscale, int32_t num_seqs, const int32_t* cu_seqlens_q,
-                           int32_t total_q, int32_t max_q_len, const int32_t* block_tables,
-                           int32_t max_blocks_per_seq, const int32_t* context_lens,
-                           int32_t max_context_len, int32_t* dev_err, void* q_out,
-                           pkv_stream_t stream)
+pkv_status pkv_rope_append_at(const pkv_cache_desc* cache, float* scales, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, int32_t in_dtype, int32_t num_heads,
+                              const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                              float mscale, int32_t num_seqs, const int32_t* cu_seqlens_q,
+                              int32_t total_q, int32_t max_q_len, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, const int32_t* context_lens,
+                              int32_t max_context_len, const int32_t* position_offsets,
+                              int32_t* dev_err, void* q_out, pkv_stream_t stream)
 {
     const bool scaled = scales != nullptr;
     pkv_status st = check_cache(cache, scaled);
@@ -209,10 +154,27 @@ pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const voi
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.context_lens = context_lens;
     p.max_context_len = max_context_len;
+    p.position_offsets = position_offsets;
     p.dev_err = dev_err;
     p.q_out = q_out;
     return from_cuda(
         pkv::launch_rope_append(p, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_rope_append(const pkv_cache_desc* cache, float* scales, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, int32_t in_dtype, int32_t num_heads,
+                           const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                           float mscale, int32_t num_seqs, const int32_t* cu_seqlens_q,
+                           int32_t total_q, int32_t max_q_len, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t max_context_len, int32_t* dev_err, void* q_out,
+                           pkv_stream_t stream)
+{
+    return pkv_rope_append_at(cache, scales, q, q_stride, k, k_stride, v, v_stride, in_dtype, num_heads,
+                              inv_freq, rot_dim, interleaved, mscale, num_seqs, cu_seqlens_q, total_q,
+                              max_q_len, block_tables, max_blocks_per_seq, context_lens,
+                              max_context_len, nullptr, dev_err, q_out, stream);
 }
 
 int32_t pkv_decode_scaled_partition_size(const pkv_cache_desc* cache, int32_t num_seqs,

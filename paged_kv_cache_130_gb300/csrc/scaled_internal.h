@@ -40,6 +40,7 @@ struct RopeParams {
     int32_t max_blocks_per_seq;
     const int32_t* context_lens;
     int32_t max_context_len;
+    const int32_t* position_offsets;   // [num_seqs], or null: position - place in the context
     int32_t* dev_err;
     void* q_out;                   // [total_q][num_heads][head_dim]
 };
@@ -55,6 +56,33 @@ int64_t decode_scaled_ctas(int32_t group, int sms);
 int64_t decode_scaled_partial_rows(int32_t group, int sms);
 // The library's choice: tokens per partition, or 0 for equal shares.
 int32_t decode_scaled_partition(const DecodeParams& p);
+
+// What the decode that adds its weights has beside DecodeParams (scratch in
+// `scores`, `whole`): weights[s][h][t] += the softmax weight of token t, summed
+// over the query heads of KV head h.
+struct DecodeExtra {
+    float* scores;                 // [num_seqs][num_kv_heads][score_tokens][pitch], log2
+    int64_t score_tokens;
+    int32_t pitch;                 // query heads of a KV head, to the next power of two
+    float* weights;
+    int64_t weights_seq;           // elements between sequences, KV heads
+    int64_t weights_head;
+    float2* whole;                 // [num_seqs][num_heads]: (maximum, 1 / sum) of items one CTA held
+};
+
+constexpr int kWeightsSeqs = 1024;     // sequences a launch takes
+
+// partition_size > 0: contexts of at most that many tokens, one launch; 0: equal
+// shares (at most kWeightsSeqs sequences).
+cudaError_t launch_decode_weights(const DecodeParams& p, const float* scales, const DecodeExtra& x,
+                                  int sms, cudaStream_t stream);
+
+// Shared prefixes (p.grp_*): ws_m, ws_l, ws_o of decode_prefix_rows rows.
+constexpr int kSharedEntries = 2048;   // groups and sequences a launch takes
+cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int sms,
+                                        cudaStream_t stream);
+int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group,
+                           int32_t max_group_size, int sms);
 
 struct ScaledPrefillParams {
     PrefillParams p;               // dtype = that of q and out
