@@ -132,9 +132,12 @@ WeightsLayout weights_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t 
     return w;
 }
 
+// The weights of a window: launches of up to kWindowSeqs sequences, which share the
+// scratch.
 struct WindowLayout {
-    pkv::WeightsPlan plan;
-    int64_t factors_off, partials_off, bytes;
+    int32_t seqs;              // of one launch
+    int32_t row_tiles, ctas;
+    int64_t info_off, partials_off, finished_off, bytes;
 };
 
 WindowLayout window_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, int32_t window,
@@ -142,14 +145,15 @@ WindowLayout window_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t nu
 {
     WindowLayout w{};
     // (a sequence has no more rows than its context)
-    const int32_t rows = window < max_context_len ? window : max_context_len;
-    w.plan = pkv::plan_weights(num_seqs, c->num_kv_heads, num_heads / c->num_kv_heads, rows,
-                               max_context_len, device_sms());
-    const int64_t items = (int64_t)num_seqs * c->num_kv_heads;
-    const int64_t per = (int64_t)w.plan.row_tiles * 128;
-    w.factors_off = round_up(items * per * c->head_dim * 2, 256);
-    w.partials_off = w.factors_off + round_up(items * per * 4, 256);
-    w.bytes = w.partials_off + round_up(items * w.plan.chunks * 2 * per * 8, 256);
+    const int64_t rows = window < max_context_len ? window : max_context_len;
+    w.seqs = num_seqs < pkv::kWindowSeqs ? num_seqs : pkv::kWindowSeqs;
+    w.row_tiles = (int32_t)((rows * (num_heads / c->num_kv_heads) + 127) / 128);
+    w.ctas = device_sms();
+    const int64_t tiles = (int64_t)w.seqs * c->num_kv_heads * w.row_tiles;
+    w.info_off = tiles * 128 * c->head_dim * 2;
+    w.partials_off = round_up(w.info_off + tiles * 260 * 4, 256);
+    w.finished_off = w.partials_off + 2 * (int64_t)w.ctas * w.row_tiles * 128 * 4;
+    w.bytes = w.finished_off + round_up(4 * (int64_t)w.seqs * c->num_kv_heads, 256);
     return w;
 }
 
@@ -262,31 +266,36 @@ pkv_status pkv_attention_weights(const pkv_cache_desc* cache, const float* scale
     p.cache_dtype = cache->cache_dtype;
     p.q = q;
     p.q_dtype = q_dtype;
-    p.num_seqs = num_seqs;
     p.num_heads = num_heads;
     p.group = num_heads / cache->num_kv_heads;
-    p.cu_seqlens_q = cu_seqlens_q;
     p.total_q = total_q;
     p.window = window < max_context_len ? window : max_context_len;
-    p.block_tables = block_tables;
     p.max_blocks_per_seq = max_blocks_per_seq;
-    p.context_lens = context_lens;
     p.max_context_len = max_context_len;
     const bool one_scale = cache->cache_dtype == PKV_FP8_E4M3 && !scaled;
     p.qk_scale_log2 = scale * kLog2E * (one_scale ? cache->k_scale : 1.f);
     if (!(fabsf(p.qk_scale_log2) < INFINITY))
         return PKV_ERR_INVALID_ARG;
-    p.chunk_tiles = wl.plan.chunk_tiles;
-    p.chunks = wl.plan.chunks;
-    p.row_tiles = wl.plan.row_tiles;
+    p.row_tiles = wl.row_tiles;
+    p.ctas = wl.ctas;
     p.q_tiles = ws;
-    p.factors = reinterpret_cast<float*>(ws + wl.factors_off);
-    p.partials = reinterpret_cast<float2*>(ws + wl.partials_off);
-    p.weights = weights;
+    p.row_info = reinterpret_cast<float*>(ws + wl.info_off);
+    p.partials = reinterpret_cast<float*>(ws + wl.partials_off);
+    p.finished = reinterpret_cast<int32_t*>(ws + wl.finished_off);
     p.weights_seq = weights_seq;
     p.weights_head = weights_head;
     p.dev_err = dev_err;
-    return from_cuda(pkv::launch_attention_weights(p, reinterpret_cast<cudaStream_t>(stream)));
+    for (int32_t s0 = 0; s0 < num_seqs; s0 += wl.seqs) {
+        p.num_seqs = num_seqs - s0 < wl.seqs ? num_seqs - s0 : wl.seqs;
+        p.cu_seqlens_q = cu_seqlens_q + s0;
+        p.block_tables = block_tables + (int64_t)s0 * max_blocks_per_seq;
+        p.context_lens = context_lens + s0;
+        p.weights = weights + s0 * weights_seq;
+        st = from_cuda(pkv::launch_attention_weights(p, reinterpret_cast<cudaStream_t>(stream)));
+        if (st != PKV_OK)
+            return st;
+    }
+    return PKV_OK;
 }
 
 size_t pkv_decode_scaled_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,

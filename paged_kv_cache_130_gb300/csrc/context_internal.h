@@ -8,16 +8,7 @@
 
 namespace pkv {
 
-// How pkv_attention_weights cuts its work: runs of `chunk_tiles` 128-key tiles,
-// `chunks` of them for the longest context; q tiles of 128 rows per KV head.
-struct WeightsPlan {
-    int32_t chunk_tiles;
-    int32_t chunks;
-    int32_t row_tiles;
-};
-
-WeightsPlan plan_weights(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t window,
-                         int32_t max_context_len, int sms);
+constexpr int kWindowSeqs = 512;       // sequences a launch of attention weights takes
 
 struct WeightsParams {
     const void* k_cache;
@@ -40,12 +31,12 @@ struct WeightsParams {
     const int32_t* context_lens;
     int32_t max_context_len;
     float qk_scale_log2;           // scale * log2(e), times the cache's one scale
-    int32_t chunk_tiles;           // the plan
-    int32_t chunks;
-    int32_t row_tiles;
+    int32_t row_tiles;             // q tiles of 128 rows of a KV head: ceil(window * group / 128)
+    int32_t ctas;                  // of a pass: one an SM
     void* q_tiles;                 // [num_seqs][num_kv_heads][row_tiles] operand tiles
-    float* factors;                // [num_seqs][num_kv_heads][row_tiles * 128]
-    float2* partials;              // [num_seqs][num_kv_heads][chunks][2][row_tiles * 128]: m, l
+    float* row_info;               // [num_seqs][num_kv_heads][row_tiles][260]: factors, -log sums, a flag
+    float* partials;               // [2 ctas][row_tiles * 128]: log sums
+    int32_t* finished;             // [num_seqs][num_kv_heads]: segments done
     float* weights;                // element (s, h, t) at s weights_seq + h weights_head + t
     int64_t weights_seq;
     int64_t weights_head;
