@@ -712,7 +712,7 @@ pkv_status pkv_attention_weights(const pkv_cache_desc* cache, const float* scale
  * workspace   pkv_decode_scaled_weights_workspace_bytes bytes, 256-byte aligned (it
  *             holds every score: 4 bytes a token and query head, the latter to the
  *             next power of two, of up to 1,024 sequences of max_context_len).
- * Launches: one kernel for contexts up to 1,024 tokens, two beyond, for every
+ * Launches: one kernel for contexts up to 1,024 tokens, three beyond, for every
  * 1,024 sequences.
  * ------------------------------------------------------------------------- */
 size_t pkv_decode_scaled_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,

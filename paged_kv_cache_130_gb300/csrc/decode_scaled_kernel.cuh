@@ -125,8 +125,9 @@ static_assert(kMinUnits / 2 > kItemUnits, "at most one CTA of an item has none o
 constexpr int kMaxBalanced = 1024;         // sequences
 
 // What the kernels do beside the plain decode.
-//   kWeights: every score goes to `scores`, and a second kernel adds each token's
-//     softmax weight, summed over the query heads of its KV head, to `weights`.
+//   kWeights: every score goes to `scores`, from which each token's softmax weight,
+//     summed over the query heads of its KV head, is added to `weights`: here where
+//     a CTA holds whole contexts, else by the kernel of decode_weights.cu.
 //   kShared: sequences [grp_begin[i], grp_begin[i + 1]) share their leading blocks.
 //     A group's prefix is read once for each `rows` rows (members x query heads of
 //     a KV head), each sequence's own tokens for its query heads; the reduce
@@ -862,58 +863,10 @@ __device__ __forceinline__ Pieces pieces_of(const Shares& sh, int64_t x, int n)
     return pc;
 }
 
-// kWeights: tokens [first, first + kWeightTokens) of one KV head of a sequence.
-constexpr int kWeightTokens = 1024;
-
-__device__ __forceinline__ void add_weights(const DecodeParams& p, const DecodeExtra& x_,
-                                            const Shares& sh, const int* sm_first, int64_t item,
-                                            int first, int rt)
-{
-    __shared__ float2 fin[kMaxGroup];          // maximum, 1 / sum
-    const int lane = threadIdx.x & 31;
-    const int s = (int)(item / p.num_kv_heads);
-    const int head = (int)(item - (int64_t)s * p.num_kv_heads);
-    const int n = sm_first[s + 1] - sm_first[s];
-    const int ctx = n > 0 ? __ldg(p.context_lens + s) : 0;
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    if (first >= ctx)
-        return;
-    const Pieces pc = pieces_of(sh, (int64_t)sm_first[s] * p.num_kv_heads + (int64_t)head * n, n);
-    for (int r = threadIdx.x >> 5; r < p.group; r += kWarps) {
-        if (pc.c0 == pc.c1) {
-            if (lane == 0)
-                fin[r] = x_.whole[(int64_t)s * p.num_heads + head * p.group + r];
-            continue;
-        }
-        float M = kNegInf, L = 0.f;
-        for (uint32_t c = pc.c0 + lane; c <= pc.c1; c += 32)
-            M = fmaxf(M, p.ws_m[pc.row(c, rt, r)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (uint32_t c = pc.c0 + lane; c <= pc.c1; c += 32) {
-            const float m = p.ws_m[pc.row(c, rt, r)];
-            L += m == kNegInf ? 0.f : exp2_fast(m - M) * p.ws_l[pc.row(c, rt, r)];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0)
-            fin[r] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
-    }
-    __syncthreads();
-    const float* sc = x_.scores + item * x_.score_tokens * x_.pitch;
-    float* w = x_.weights + s * x_.weights_seq + head * x_.weights_head;
-    const int end = min(ctx, first + kWeightTokens);
-    for (int tok = first + threadIdx.x; tok < end; tok += kWarps * 32)
-        w[tok] += token_weight(sc + (int64_t)tok * x_.pitch, p.group, x_.pitch, fin);
-}
-
 // Merge of the partials of the equal shares: one warp per (sequence, query
 // head).  Items that one CTA held whole are left alone (kShared: unless the row
 // has a prefix); sequences without tokens (or with an unusable length) get zeros.
-// kWeights: the CTAs behind add the weights, kWeightTokens tokens of an item each.
+// kWeights: a row's maximum and 1 / sum are filed too.
 constexpr int kReduceRows = kWarps;          // (scan_units wants kWarps warps)
 
 template <int QT, int D, int MODE>
@@ -927,15 +880,6 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     const Shares sh = shares_of(p, sm_first[entries], grid);
     const int lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
-    if constexpr (MODE == kWeights) {
-        const int64_t behind = (int64_t)blockIdx.x - (rows + kReduceRows - 1) / kReduceRows;
-        if (behind >= 0) {
-            const int64_t items = (int64_t)p.num_seqs * p.num_kv_heads;
-            add_weights(p, x_, sh, sm_first, behind % items, (int)(behind / items) * kWeightTokens,
-                        rows_per_partial);
-            return;
-        }
-    }
     const int64_t row = (int64_t)blockIdx.x * kReduceRows + (threadIdx.x >> 5);
     if (row >= rows)
         return;
@@ -1034,6 +978,9 @@ __global__ void __launch_bounds__(kReduceRows * 32)
             sum(pre, rpre, wpre);
         if (has_own)
             sum(own, r, wown);
+        if constexpr (MODE == kWeights)
+            if (lane == 0)
+                x_.whole[row] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row * D + lane * DPL;
