@@ -88,10 +88,12 @@ void place(pkv::DecodeParams& p, const Partials& w, char* ws)
     p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
 }
 
-Partials shared_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, int32_t max_group_size)
+Partials shared_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, int32_t num_groups,
+                       int32_t max_group_size)
 {
-    return partials(pkv::decode_prefix_rows(num_seqs, num_heads, num_heads / c->num_kv_heads, max_group_size,
-                                            device_sms()),
+    const int32_t members = max_group_size < num_seqs ? max_group_size : num_seqs;
+    return partials(pkv::decode_prefix_rows(num_seqs, num_heads, num_heads / c->num_kv_heads, num_groups,
+                                            members, device_sms()),
                     c->head_dim);
 }
 
@@ -168,8 +170,10 @@ size_t pkv_decode_scaled_shared_prefix_workspace_bytes(const pkv_cache_desc* cac
     if (!sizes_known(cache, num_seqs, num_heads, max_context_len) || num_groups < 0 || max_group_size < 0)
         return 0;
     const size_t plain = pkv_decode_scaled_workspace_bytes(cache, num_seqs, num_heads, max_context_len, 0);
-    const size_t shared = (size_t)shared_layout(cache, num_seqs, num_heads, max_group_size).bytes;
-    return num_groups == 0 || plain > shared ? plain : shared;
+    if (num_groups == 0 || max_group_size == 0 || num_heads / cache->num_kv_heads > 16)
+        return plain;
+    const size_t shared = (size_t)shared_layout(cache, num_seqs, num_heads, num_groups, max_group_size).bytes;
+    return plain > shared ? plain : shared;
 }
 
 pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
@@ -202,7 +206,7 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
         context_lens == nullptr || block_tables == nullptr || group_begin == nullptr ||
         group_prefix_blocks == nullptr || !aligned(q, 16) || !aligned(out, 16))
         return PKV_ERR_INVALID_ARG;
-    const Partials wl = shared_layout(cache, num_seqs, num_heads, max_group_size);
+    const Partials wl = shared_layout(cache, num_seqs, num_heads, num_groups, max_group_size);
     if (workspace == nullptr || !aligned(workspace, 256) || (int64_t)workspace_bytes < wl.bytes)
         return PKV_ERR_WORKSPACE;
     pkv::DecodeParams p =

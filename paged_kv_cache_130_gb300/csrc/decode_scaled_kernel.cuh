@@ -234,7 +234,7 @@ __device__ __forceinline__ int entry_units(const DecodeParams& p, int e, int rt,
 {
     if (e < p.num_groups) {
         const Group g = group_at(p, e, flag);
-        return g.prefix > 0 ? (ceil_div_i(g.prefix, kUnit) + kItemUnits) * tiles_of(p, g, rt) : 0;
+        return g.prefix > 0 && p.prefix_partition == 0 ? (ceil_div_i(g.prefix, kUnit) + kItemUnits) * tiles_of(p, g, rt) : 0;
     }
     const int s = e - p.num_groups;
     const int ctx = __ldg(p.context_lens + s);
@@ -361,8 +361,11 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     const int t = lane & 3;
     const int G = p.group;
 
-    // what comes before in the stream may still write q, the cache and the tables
-    pdl_wait_primary();
+    // what comes before in the stream may still write q, the cache and the tables;
+    // the kernel of the prefixes only writes their partials: it is waited for at the end
+    const bool beside = MODE == kShared && p.prefix_partition > 0;
+    if (!beside)
+        pdl_wait_primary();
     pdl_launch_dependents();
 
     // BAL: units left of the CTA's share, and where it stands: unit u0 of KV
@@ -379,8 +382,11 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
         scan_units<MODE>(p, sm_first, RT, blockIdx.x == 0);
         const Shares sh = shares_of(p, sm_first[entries], gridDim.x);
-        if (blockIdx.x >= sh.ctas)
+        if (blockIdx.x >= sh.ctas) {
+            if (beside)
+                pdl_wait_primary();
             return;
+        }
         const int64_t at = sh.begin(blockIdx.x);
         left = sh.begin(blockIdx.x + 1) - at;
         int hi = entries;                      // the last s with first[s] Hkv <= at
@@ -436,9 +442,9 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         whole = u0 <= kItemUnits && u1 == n;
         direct = whole && !prefix;
         // pieces lie behind one another, two a CTA; behind them the rows of whole
-        // items: the prefixes' as in q, then the own tokens'
+        // items: the own tokens' as in q, then the prefixes'
         prow = whole ? 2 * (int64_t)gridDim.x * RT +
-                           (e < p.num_groups ? 0 : (int64_t)p.num_seqs * p.num_heads)
+                           (e < p.num_groups ? (int64_t)p.num_seqs * p.num_heads : 0)
                      : (2 * (int64_t)blockIdx.x + (u0 <= kItemUnits ? 1 : 0)) * RT;
         left -= u1 - u0;
         u0 = 0;
@@ -842,6 +848,8 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     // (the next item's q is filed once every warp is past the barrier above, its
     // states once every warp is past the one behind q)
     }
+    if (beside)
+        pdl_wait_primary();
 }
 
 // The partials of one item of n units from unit x on: which CTAs filed them.
@@ -903,7 +911,8 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         if (!bad && pre > 0) {
             const int tiles = tiles_of(p, g, rows_per_partial);
             const int rr = (s - g.begin) * p.group + r;
-            npre = ceil_div_i(pre, kUnit) + kItemUnits;
+            npre = p.prefix_partition > 0 ? ceil_div_i(pre, p.prefix_partition)
+                                          : ceil_div_i(pre, kUnit) + kItemUnits;
             rpre = rr % rows_per_partial;
             xpre = (int64_t)sm_first[i] * p.num_kv_heads +
                    ((int64_t)head * tiles + rr / rows_per_partial) * npre;
@@ -942,13 +951,15 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         const bool has_own = n > 0;
         if (has_own)
             own = pieces_of(sh, (int64_t)sm_first[e] * p.num_kv_heads + (int64_t)head * n, n);
-        if (npre > 0)
+        // (prefixes with a kernel of their own: npre runs, each with its rows)
+        const bool runs = MODE == kShared && p.prefix_partition > 0;
+        if (npre > 0 && !runs)
             pre = pieces_of(sh, xpre, npre);
-        else if (own.c0 == own.c1)
+        if (npre == 0 && own.c0 == own.c1)
             return;
         // rows of whole items: behind the pieces
-        const int64_t wpre = 2 * grid * rows_per_partial + row;
-        const int64_t wown = wpre + rows;
+        const int64_t wown = 2 * grid * rows_per_partial + row;
+        const int64_t wpre = wown + rows;
         float M = kNegInf;
         auto most = [&](const Pieces& pc, int rr, int64_t whole) {
             if (pc.c0 == pc.c1) {
@@ -967,15 +978,23 @@ __global__ void __launch_bounds__(kReduceRows * 32)
             for (uint32_t c = pc.c0; c <= pc.c1; ++c)
                 add(pc.row(c, rows_per_partial, rr), M);
         };
-        if (npre > 0)
+        if (runs)
+            for (int i = lane; i < npre; i += 32)
+                M = fmaxf(M, p.ws_m[wpre + i * rows]);
+        else if (npre > 0)
             most(pre, rpre, wpre);
         if (has_own)
             most(own, r, wown);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (npre > 0)
+        if (runs) {
+#pragma unroll 4
+            for (int i = 0; i < npre; ++i)
+                add(wpre + i * rows, M);
+        } else if (npre > 0) {
             sum(pre, rpre, wpre);
+        }
         if (has_own)
             sum(own, r, wown);
         if constexpr (MODE == kWeights)

@@ -1,35 +1,125 @@
 // decode_scaled_prefix.cu -- decode over a scaled cache for groups of sequences that
 // share their leading blocks.
 //
-// Attention over [0, c) splits at the end P of the shared prefix.  Both parts are
-// items of the equal shares of decode_scaled_kernel.cuh: a prefix for every 8 or 16
-// rows (members x query heads of a KV head) of its group, read for all of them
-// at once, and each sequence's tokens from P on.  The reduce merges what belongs
-// to a row.
+// Attention over [0, c) splits at the end P of the shared prefix.  Few rows (members
+// x query heads of a KV head): both parts are items of the equal shares of
+// decode_scaled_kernel.cuh: a prefix for every 8 or 16 rows of its group, read for
+// all of them at once, and each sequence's tokens from P on.  Many rows: the
+// prefixes go to the tensor-memory kernel of prefill_scaled_kernel.cuh, 256 rows a
+// CTA and the keys in runs, beside which the shares hold the own tokens only.  The
+// reduce merges what belongs to a row.
 #include <cuda_runtime.h>
 
 #include "decode_scaled_kernel.cuh"
+#include "prefill_scaled_kernel.cuh"
 
 namespace pkv {
 namespace {
 
 using namespace dsk;
 
+constexpr int kKeys = pfs::kKeys;
+constexpr int kManyRows = 32;              // rows of a group beyond which prefixes have their own kernel
+constexpr int kMinRun = 4 * kKeys;         // keys of a CTA of it
+
+bool many_rows(int32_t group, int32_t max_group_size) { return (int64_t)group * max_group_size > kManyRows; }
+
+// Rows of an item of the shares.
 int rows_of(int32_t group, int32_t max_group_size)
 {
-    return group > 8 || (int64_t)group * max_group_size > 8 ? 16 : 8;
+    const int64_t rows = many_rows(group, max_group_size) ? group : (int64_t)group * max_group_size;
+    return group > 8 || rows > 8 ? 16 : 8;
+}
+
+// CTAs of one run over every group's prefix, and the most runs: what fills the GPU
+// once.
+int64_t ctas_of_run(int32_t num_groups, int32_t num_kv_heads, int32_t group, int32_t max_group_size)
+{
+    const int span = 2 * (pfs::kRows / group);
+    return (int64_t)num_groups * num_kv_heads * ((max_group_size + span - 1) / span);
+}
+
+int64_t most_runs(int32_t num_groups, int32_t num_kv_heads, int32_t group, int32_t max_group_size, int sms)
+{
+    const int64_t n = sms / ctas_of_run(num_groups, num_kv_heads, group, max_group_size);
+    return n < 1 ? 1 : n;
+}
+
+// The prefixes' own kernel.
+template <int QT, int D, int BS>
+cudaError_t run_prefixes(const DecodeParams& p, const float* scales, int64_t first_row, cudaStream_t stream)
+{
+    using L = pfs::Layout<D>;
+    auto kern = pfs::prefill_scaled_kernel<QT, D, BS, true>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
+        if (e != cudaSuccess)
+            return e;
+        configured[dev] = true;
+    }
+    ScaledPrefillParams sp{};
+    sp.p.k_cache = p.k_cache;
+    sp.p.v_cache = p.v_cache;
+    sp.p.num_blocks = p.num_blocks;
+    sp.p.num_kv_heads = p.num_kv_heads;
+    sp.p.block_size = p.block_size;
+    sp.p.head_dim = p.head_dim;
+    sp.p.dtype = p.q_dtype;
+    sp.p.q = p.q;
+    sp.p.num_seqs = p.num_seqs;
+    sp.p.num_heads = p.num_heads;
+    sp.p.group = p.group;
+    sp.p.block_tables = p.block_tables;
+    sp.p.max_blocks_per_seq = p.max_blocks_per_seq;
+    sp.p.qk_scale_log2 = p.qk_scale_log2;
+    sp.p.dev_err = p.dev_err;
+    sp.scales = scales;
+    PrefixParams px{};
+    px.grp_begin = p.grp_begin;
+    px.grp_prefix_blocks = p.grp_prefix_blocks;
+    px.num_groups = p.num_groups;
+    px.max_group_size = p.max_group_size;
+    px.max_prefix_blocks = p.max_prefix_blocks;
+    px.run = p.prefix_partition;
+    px.first_row = first_row;
+    px.ws_m = p.ws_m;
+    px.ws_l = p.ws_l;
+    px.ws_o = p.ws_o;
+    const int64_t runs = ((int64_t)p.max_prefix_blocks * p.block_size + px.run - 1) / px.run;
+    const int64_t ctas = runs * ctas_of_run(p.num_groups, p.num_kv_heads, p.group, p.max_group_size);
+    if (ctas > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    kern<<<(unsigned)ctas, pfs::kThreads, L::alloc, stream>>>(sp, px);
+    return cudaGetLastError();
 }
 
 template <int QT, int D, int BS, int NNT>
-cudaError_t run(const DecodeParams& p, const float* scales, int sms, cudaStream_t stream)
+cudaError_t run(const DecodeParams& p0, const float* scales, int sms, cudaStream_t stream)
 {
+    DecodeParams p = p0;
     const int64_t ctas = decode_scaled_ctas(8 * NNT, sms);
+    const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
+    if (many_rows(p.group, p.max_group_size)) {
+        const int64_t n = most_runs(p.num_groups, p.num_kv_heads, p.group, p.max_group_size, sms);
+        const int64_t tiles = ((int64_t)p.max_prefix_blocks * BS + kKeys - 1) / kKeys;
+        const int64_t run = (tiles + n - 1) / n * kKeys;
+        p.prefix_partition = (int32_t)(run < kMinRun ? kMinRun : run);
+        cudaError_t e = run_prefixes<QT, D, BS>(p, scales, 2 * ctas * 8 * NNT + rows, stream);
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaError_t e = launch_early(decode_scaled_kernel<QT, D, BS, NNT, true, kShared>, ctas,
                                  kWarps * 32, stream, p, reinterpret_cast<const float2*>(scales),
                                  DecodeExtra{});
     if (e != cudaSuccess)
         return e;
-    const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
     return launch_early(reduce_shares_kernel<QT, D, kShared>, (rows + kReduceRows - 1) / kReduceRows,
                         kReduceRows * 32, stream, p, ctas, 8 * NNT, DecodeExtra{});
 }
@@ -73,13 +163,16 @@ cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scal
                              : by_dim<kBF16>(p, scales, sms, stream);
 }
 
-// Two pieces a CTA, and the rows of items that one CTA held whole, prefixes and
-// own tokens.
-int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group,
+// Two pieces a CTA, the rows of sequences whose own tokens one CTA held, those of the
+// prefixes: of what one CTA held, or of every run.
+int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t num_groups,
                            int32_t max_group_size, int sms)
 {
     const int rt = rows_of(group, max_group_size);
-    return 2 * decode_scaled_ctas(rt, sms) * rt + 2 * (int64_t)num_seqs * num_heads;
+    const int64_t runs = many_rows(group, max_group_size)
+                             ? most_runs(num_groups, num_heads / group, group, max_group_size, sms)
+                             : 1;
+    return 2 * decode_scaled_ctas(rt, sms) * rt + (1 + runs) * (int64_t)num_seqs * num_heads;
 }
 
 }  // namespace pkv

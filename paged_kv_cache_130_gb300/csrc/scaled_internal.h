@@ -81,12 +81,28 @@ cudaError_t launch_decode_weights(const DecodeParams& p, const float* scales, co
 constexpr int kSharedEntries = 2048;   // groups and sequences a launch takes
 cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int sms,
                                         cudaStream_t stream);
-int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group,
+int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t num_groups,
                            int32_t max_group_size, int sms);
 
 struct ScaledPrefillParams {
     PrefillParams p;               // dtype = that of q and out
     const float* scales;
+};
+
+// The prefixes that groups of sequences share, as launch_prefill_scaled's kernel
+// takes them: partials of the rows of q over runs of `run` keys, the rows of run i
+// from first_row + i num_seqs num_heads on.
+struct PrefixParams {
+    const int32_t* grp_begin;
+    const int32_t* grp_prefix_blocks;
+    int32_t num_groups;
+    int32_t max_group_size;
+    int32_t max_prefix_blocks;
+    int32_t run;                   // a multiple of 128
+    int64_t first_row;
+    float* ws_m;
+    float* ws_l;
+    float* ws_o;
 };
 
 cudaError_t launch_prefill_scaled(const ScaledPrefillParams& p, cudaStream_t stream);

@@ -121,6 +121,11 @@ SHARED = [
     (W.F16, 3, 1, 128, 16, [(40, [10] * 11), (1, [700, 3])]),
     (W.BF16, 5, 5, 128, 16, [(1, [1] * 9)] * 7),
     (W.F16, 14, 2, 64, 8, [(130, [5, 300, 1]), (64, [64] * 4)]),
+    # more rows than 32: prefixes by a kernel of their own, in runs of keys
+    (W.F16, 8, 2, 64, 16, [(150, [3] * 20), (0, [5]), (70, [1, 200] + [2] * 15)]),
+    (W.BF16, 16, 1, 128, 32, [(40, [7, 0, 0, 33, 1]), (1, [1] * 3)]),
+    (W.BF16, 8, 1, 128, 8, [(200, [4] * 40), (17, [9] * 33)]),              # two CTAs' rows
+    (W.F16, 3, 1, 128, 16, [(65, [2] * 90)]),
 ]
 
 
