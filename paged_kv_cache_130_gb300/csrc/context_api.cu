@@ -67,17 +67,18 @@ pkv::DecodeParams decode_params(const pkv_cache_desc* cache, const void* q, int3
     return p;
 }
 
-// Scratch of m, l and o partials: `rows` rows.
+// Scratch of m, l and o partials: `rows` rows, and `more` bytes.
 struct Partials {
-    int64_t l_off, o_off, bytes;
+    int64_t l_off, o_off, more_off, bytes;
 };
 
-Partials partials(int64_t rows, int32_t head_dim)
+Partials partials(int64_t rows, int32_t head_dim, int64_t more = 0)
 {
     Partials w{};
     w.l_off = round_up(4 * rows, 256);
     w.o_off = 2 * w.l_off;
-    w.bytes = w.o_off + round_up(4 * rows * head_dim, 256);
+    w.more_off = w.o_off + round_up(4 * rows * head_dim, 256);
+    w.bytes = w.more_off + more;
     return w;
 }
 
@@ -88,13 +89,14 @@ void place(pkv::DecodeParams& p, const Partials& w, char* ws)
     p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
 }
 
+// (behind them: units before each group and sequence)
 Partials shared_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, int32_t num_groups,
                        int32_t max_group_size)
 {
     const int32_t members = max_group_size < num_seqs ? max_group_size : num_seqs;
     return partials(pkv::decode_prefix_rows(num_seqs, num_heads, num_heads / c->num_kv_heads, num_groups,
                                             members, device_sms()),
-                    c->head_dim);
+                    c->head_dim, round_up(4 * ((int64_t)num_groups + num_seqs + 1), 256));
 }
 
 // The decode that adds its weights: contexts up to kOnePass tokens are one CTA's
@@ -218,7 +220,8 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
     p.num_groups = num_groups;
     p.max_group_size = max_group_size < num_seqs ? max_group_size : num_seqs;
     p.max_prefix_blocks = max_prefix_blocks;
-    return from_cuda(pkv::launch_decode_scaled_prefix(p, scales, device_sms(),
+    int32_t* first = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) + wl.more_off);
+    return from_cuda(pkv::launch_decode_scaled_prefix(p, scales, first, device_sms(),
                                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -228,22 +228,56 @@ __device__ __forceinline__ int own_begin(const DecodeParams& p, int s, int ctx, 
     return g.prefix;
 }
 
-// Units (of one KV head) of entry e of a shared batch: the groups' prefixes, then
-// the sequences' own tokens.
-__device__ __forceinline__ int entry_units(const DecodeParams& p, int e, int rt, bool flag)
+// An entry of a shared batch: the groups' prefixes, then the sequences' own tokens.
+// The item of a KV head begins at token `from` (of sequence `from`: a prefix) and ends
+// before token `end`.
+struct Entry {
+    int from, end;
+    int rows;                  // members x query heads of a KV head; 0: no item
+};
+
+__device__ __forceinline__ Entry entry_at(const DecodeParams& p, int e, const int* begins, bool flag)
 {
+    Entry en{0, 0, 0};
     if (e < p.num_groups) {
         const Group g = group_at(p, e, flag);
-        return g.prefix > 0 && p.prefix_partition == 0 ? (ceil_div_i(g.prefix, kUnit) + kItemUnits) * tiles_of(p, g, rt) : 0;
+        if (g.prefix > 0 && p.prefix_partition == 0)
+            en = Entry{g.begin, g.prefix, g.members * p.group};
+        return en;
     }
     const int s = e - p.num_groups;
     const int ctx = __ldg(p.context_lens + s);
-    const int i = group_of(p, s);
+    int i = 0, hi = p.num_groups;              // the group: the last that starts at or before s
+    while (hi - i > 1) {
+        const int mid = (i + hi) >> 1;
+        if (begins[mid] <= s)
+            i = mid;
+        else
+            hi = mid;
+    }
     bool bad;
     const int pre = own_begin(p, s, ctx, i, group_at(p, i, false), bad);
     if (bad && flag)
         flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
-    return bad || ctx == pre ? 0 : ceil_div_i(ctx - pre, kUnit) + kItemUnits;
+    if (!bad && ctx > pre)
+        en = Entry{pre, ctx, p.group};
+    return en;
+}
+
+// Its units (of one KV head), with all the row tiles of a prefix.
+__device__ __forceinline__ int entry_units(const DecodeParams& p, int e, const Entry& en, int rt)
+{
+    if (en.rows == 0)
+        return 0;
+    return e < p.num_groups ? (ceil_div_i(en.end, kUnit) + kItemUnits) * ceil_div_i(en.rows, rt)
+                            : ceil_div_i(en.end - en.from, kUnit) + kItemUnits;
+}
+
+// Shared memory of a shared batch beside the kernel's own: its entries, and the
+// groups' first members.
+inline size_t shared_entries_bytes(int num_groups, int num_seqs)
+{
+    return ((size_t)num_groups + num_seqs) * sizeof(Entry) + ((size_t)num_groups + 1) * sizeof(int);
 }
 
 // first[e] = units before entry e (of one KV head), first[entries] = all; an
@@ -251,7 +285,8 @@ __device__ __forceinline__ int entry_units(const DecodeParams& p, int e, int rt,
 // warps.  Every thread takes a run of up to max_entries / (32 kWarps) entries, so
 // that the lengths cost one round trip.
 template <int MODE>
-__device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, int rt, bool flag)
+__device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, int rt, bool flag,
+                                           Entry* table = nullptr)
 {
     constexpr int kRun = max_entries<MODE>() / (32 * kWarps);
     const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
@@ -262,11 +297,25 @@ __device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, in
     const int s0 = threadIdx.x * per;
     int v[kRun];
     int sum = 0;
+    int* begins = reinterpret_cast<int*>(table + entries);
+    if constexpr (MODE == kShared) {
+        for (int i = threadIdx.x; i <= p.num_groups; i += 32 * kWarps)
+            begins[i] = __ldg(p.grp_begin + i);
+        __syncthreads();
+    }
 #pragma unroll
-    for (int i = 0; i < kRun; ++i)
-        v[i] = i >= per || s0 + i >= entries
-                   ? 0
-                   : (MODE == kShared ? entry_units(p, s0 + i, rt, flag) : units_of(p, s0 + i, flag));
+    for (int i = 0; i < kRun; ++i) {
+        v[i] = 0;
+        if (i < per && s0 + i < entries) {
+            if constexpr (MODE == kShared) {
+                const Entry en = entry_at(p, s0 + i, begins, flag);
+                table[s0 + i] = en;
+                v[i] = entry_units(p, s0 + i, en, rt);
+            } else {
+                v[i] = units_of(p, s0 + i, flag);
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kRun; ++i)
         sum += v[i];
@@ -374,13 +423,18 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     int64_t left = 1;
     int bal_s = 0, bal_h = 0, u0 = 0;
     [[maybe_unused]] int tiles = 1, bal_n = 0;
+    extern __shared__ int sm_dyn[];
+    [[maybe_unused]] Entry* table_e = reinterpret_cast<Entry*>(sm_dyn);    // kShared
     [[maybe_unused]] auto enter = [&](int e) {
-        tiles = e < p.num_groups ? tiles_of(p, group_at(p, e, false), RT) : 1;
+        tiles = e < p.num_groups ? ceil_div_i(table_e[e].rows, RT) : 1;
         bal_n = (sm_first[e + 1] - sm_first[e]) / tiles;
     };
     if constexpr (BAL) {
         const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
-        scan_units<MODE>(p, sm_first, RT, blockIdx.x == 0);
+        scan_units<MODE>(p, sm_first, RT, blockIdx.x == 0, table_e);
+        if (MODE == kShared && blockIdx.x == 0)        // for the kernel behind
+            for (int i = threadIdx.x; i <= entries; i += kWarps * 32)
+                x_.first[i] = sm_first[i];
         const Shares sh = shares_of(p, sm_first[entries], gridDim.x);
         if (blockIdx.x >= sh.ctas) {
             if (beside)
@@ -420,23 +474,18 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         const int u1 = (int)min((int64_t)n, u0 + left);
         const int b = max(u0 - kItemUnits, 0) * kUnit;
         head = bal_h / tiles;
-        int end;
+        const Entry en = table_e[e];
+        const int end = en.end;
         bool prefix = e < p.num_groups;
         if (prefix) {
-            const Group g = group_at(p, e, false);
             rr0 = (bal_h - head * tiles) * RT;
-            s = g.begin;
-            nrows = min(RT, g.members * G - rr0);
+            s = en.from;
+            nrows = min(RT, en.rows - rr0);
             t_begin = b;
-            end = g.prefix;
         } else {
             s = e - p.num_groups;
-            end = __ldg(p.context_lens + s);
-            const int i = group_of(p, s);
-            bool bad;
-            const int pre = own_begin(p, s, end, i, group_at(p, i, false), bad);
-            t_begin = pre + b;
-            prefix = pre > 0;
+            t_begin = en.from + b;
+            prefix = en.from > 0;
         }
         t_end = min(end, t_begin - b + (u1 - kItemUnits) * kUnit);
         whole = u0 <= kItemUnits && u1 == n;
@@ -882,10 +931,13 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     reduce_shares_kernel(const DecodeParams p, int64_t grid, int rows_per_partial, const DecodeExtra x_)
 {
     constexpr int DPL = D / 32;
-    __shared__ int sm_first[max_entries<MODE>() + 1];
-    scan_units<MODE>(p, sm_first, rows_per_partial, false);
+    __shared__ int sm_first[MODE == kShared ? 1 : kMaxBalanced + 1];
+    const int* first = sm_first;               // units before each entry
+    if constexpr (MODE == kShared)
+        first = x_.first;                      // (filed by the kernel before)
+    else
+        scan_units<MODE>(p, sm_first, rows_per_partial, false);
     const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
-    const Shares sh = shares_of(p, sm_first[entries], grid);
     const int lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
     const int64_t row = (int64_t)blockIdx.x * kReduceRows + (threadIdx.x >> 5);
@@ -896,11 +948,10 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     const int head = hq / p.group;
     int r = hq - head * p.group;
     const int e = MODE == kShared ? p.num_groups + s : s;
-    const int n = sm_first[e + 1] - sm_first[e];
-    // kShared: the prefix's item, if the row has one
-    [[maybe_unused]] int npre = 0, rpre = 0;
-    [[maybe_unused]] int64_t xpre = 0;
-    bool zero = n == 0;
+    // kShared: the prefix's item (item number ipre of group gpre), if the row has one
+    [[maybe_unused]] int npre = 0, rpre = 0, gpre = 0;
+    [[maybe_unused]] int64_t ipre = 0;
+    bool zero = false;
     if constexpr (MODE == kShared) {
         const int ctx = __ldg(p.context_lens + s);
         const int i = group_of(p, s);
@@ -914,8 +965,8 @@ __global__ void __launch_bounds__(kReduceRows * 32)
             npre = p.prefix_partition > 0 ? ceil_div_i(pre, p.prefix_partition)
                                           : ceil_div_i(pre, kUnit) + kItemUnits;
             rpre = rr % rows_per_partial;
-            xpre = (int64_t)sm_first[i] * p.num_kv_heads +
-                   ((int64_t)head * tiles + rr / rows_per_partial) * npre;
+            gpre = i;
+            ipre = (int64_t)head * tiles + rr / rows_per_partial;
             // a table that differs inside the prefix: the first member's is used
             if (hq == 0 && p.dev_err != nullptr) {
                 const int32_t* a = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
@@ -933,6 +984,10 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     float L = 0.f;
     pdl_wait_primary();
     pdl_launch_dependents();
+    const int n = first[e + 1] - first[e];
+    const Shares sh = shares_of(p, first[entries], grid);
+    if constexpr (MODE != kShared)
+        zero = n == 0;
     auto add = [&](int64_t pr, float M) {
         const float m = p.ws_m[pr];
         const float f = m == kNegInf ? 0.f : exp2_fast(m - M);
@@ -950,11 +1005,11 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         Pieces own{0, 0}, pre{0, 0};
         const bool has_own = n > 0;
         if (has_own)
-            own = pieces_of(sh, (int64_t)sm_first[e] * p.num_kv_heads + (int64_t)head * n, n);
+            own = pieces_of(sh, (int64_t)first[e] * p.num_kv_heads + (int64_t)head * n, n);
         // (prefixes with a kernel of their own: npre runs, each with its rows)
         const bool runs = MODE == kShared && p.prefix_partition > 0;
         if (npre > 0 && !runs)
-            pre = pieces_of(sh, xpre, npre);
+            pre = pieces_of(sh, (int64_t)first[gpre] * p.num_kv_heads + ipre * npre, npre);
         if (npre == 0 && own.c0 == own.c1)
             return;
         // rows of whole items: behind the pieces
@@ -1012,14 +1067,15 @@ __global__ void __launch_bounds__(kReduceRows * 32)
 // The kernels here start while what precedes them in the stream ends, and wait
 // for it before they read anything it may write.
 template <class... Args>
-cudaError_t launch_early(void (*kern)(Args...), int64_t ctas, int threads, cudaStream_t stream,
-                         Args... args)
+cudaError_t launch_early_smem(void (*kern)(Args...), int64_t ctas, int threads, size_t smem,
+                              cudaStream_t stream, Args... args)
 {
     if (ctas > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1027,6 +1083,13 @@ cudaError_t launch_early(void (*kern)(Args...), int64_t ctas, int threads, cudaS
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <class... Args>
+cudaError_t launch_early(void (*kern)(Args...), int64_t ctas, int threads, cudaStream_t stream,
+                         Args... args)
+{
+    return launch_early_smem(kern, ctas, threads, 0, stream, args...);
 }
 
 }  // namespace dsk

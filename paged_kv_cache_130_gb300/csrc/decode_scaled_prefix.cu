@@ -101,7 +101,7 @@ cudaError_t run_prefixes(const DecodeParams& p, const float* scales, int64_t fir
 }
 
 template <int QT, int D, int BS, int NNT>
-cudaError_t run(const DecodeParams& p0, const float* scales, int sms, cudaStream_t stream)
+cudaError_t run(const DecodeParams& p0, const float* scales, int32_t* first, int sms, cudaStream_t stream)
 {
     DecodeParams p = p0;
     const int64_t ctas = decode_scaled_ctas(8 * NNT, sms);
@@ -115,43 +115,59 @@ cudaError_t run(const DecodeParams& p0, const float* scales, int sms, cudaStream
         if (e != cudaSuccess)
             return e;
     }
-    cudaError_t e = launch_early(decode_scaled_kernel<QT, D, BS, NNT, true, kShared>, ctas,
-                                 kWarps * 32, stream, p, reinterpret_cast<const float2*>(scales),
-                                 DecodeExtra{});
+    DecodeExtra x{};
+    x.first = first;
+    auto kern = decode_scaled_kernel<QT, D, BS, NNT, true, kShared>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)shared_entries_bytes(kSharedEntries, 1));
+        if (e != cudaSuccess)
+            return e;
+        configured[dev] = true;
+    }
+    e = launch_early_smem(kern, ctas, kWarps * 32, shared_entries_bytes(p.num_groups, p.num_seqs), stream, p,
+                          reinterpret_cast<const float2*>(scales), x);
     if (e != cudaSuccess)
         return e;
     return launch_early(reduce_shares_kernel<QT, D, kShared>, (rows + kReduceRows - 1) / kReduceRows,
-                        kReduceRows * 32, stream, p, ctas, 8 * NNT, DecodeExtra{});
+                        kReduceRows * 32, stream, p, ctas, 8 * NNT, x);
 }
 
 template <int QT, int D, int BS>
-cudaError_t by_rows(const DecodeParams& p, const float* scales, int sms, cudaStream_t st)
+cudaError_t by_rows(const DecodeParams& p, const float* scales, int32_t* first, int sms, cudaStream_t st)
 {
-    return rows_of(p.group, p.max_group_size) == 8 ? run<QT, D, BS, 1>(p, scales, sms, st)
-                     : run<QT, D, BS, 2>(p, scales, sms, st);
+    return rows_of(p.group, p.max_group_size) == 8 ? run<QT, D, BS, 1>(p, scales, first, sms, st)
+                     : run<QT, D, BS, 2>(p, scales, first, sms, st);
 }
 
 template <int QT, int D>
-cudaError_t by_block(const DecodeParams& p, const float* scales, int sms, cudaStream_t st)
+cudaError_t by_block(const DecodeParams& p, const float* scales, int32_t* first, int sms, cudaStream_t st)
 {
     switch (p.block_size) {
-    case 8: return by_rows<QT, D, 8>(p, scales, sms, st);
-    case 16: return by_rows<QT, D, 16>(p, scales, sms, st);
-    case 32: return by_rows<QT, D, 32>(p, scales, sms, st);
+    case 8: return by_rows<QT, D, 8>(p, scales, first, sms, st);
+    case 16: return by_rows<QT, D, 16>(p, scales, first, sms, st);
+    case 32: return by_rows<QT, D, 32>(p, scales, first, sms, st);
     default: return cudaErrorNotSupported;
     }
 }
 
 template <int QT>
-cudaError_t by_dim(const DecodeParams& p, const float* scales, int sms, cudaStream_t st)
+cudaError_t by_dim(const DecodeParams& p, const float* scales, int32_t* first, int sms, cudaStream_t st)
 {
-    return p.head_dim == 128 ? by_block<QT, 128>(p, scales, sms, st)
-                             : by_block<QT, 64>(p, scales, sms, st);
+    return p.head_dim == 128 ? by_block<QT, 128>(p, scales, first, sms, st)
+                             : by_block<QT, 64>(p, scales, first, sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int sms,
+cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int32_t* first, int sms,
                                         cudaStream_t stream)
 {
     if (p.num_seqs <= 0)
@@ -159,8 +175,8 @@ cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scal
     if (p.group < 1 || p.group > kMaxGroup || p.num_groups < 1 ||
         (int64_t)p.num_groups + p.num_seqs > kSharedEntries)
         return cudaErrorNotSupported;
-    return p.q_dtype == kF16 ? by_dim<kF16>(p, scales, sms, stream)
-                             : by_dim<kBF16>(p, scales, sms, stream);
+    return p.q_dtype == kF16 ? by_dim<kF16>(p, scales, first, sms, stream)
+                             : by_dim<kBF16>(p, scales, first, sms, stream);
 }
 
 // Two pieces a CTA, the rows of sequences whose own tokens one CTA held, those of the

@@ -68,6 +68,7 @@ struct DecodeExtra {
     int64_t weights_seq;           // elements between sequences, KV heads
     int64_t weights_head;
     float2* whole;                 // [num_seqs][num_heads]: (maximum, 1 / sum) of items one CTA held
+    int32_t* first;                // shared prefixes: units before each group and sequence
 };
 
 constexpr int kWeightsSeqs = 1024;     // sequences a launch takes
@@ -77,9 +78,10 @@ constexpr int kWeightsSeqs = 1024;     // sequences a launch takes
 cudaError_t launch_decode_weights(const DecodeParams& p, const float* scales, const DecodeExtra& x,
                                   int sms, cudaStream_t stream);
 
-// Shared prefixes (p.grp_*): ws_m, ws_l, ws_o of decode_prefix_rows rows.
+// Shared prefixes (p.grp_*): ws_m, ws_l, ws_o of decode_prefix_rows rows, `first` of
+// one more entry than groups and sequences.
 constexpr int kSharedEntries = 2048;   // groups and sequences a launch takes
-cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int sms,
+cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int32_t* first, int sms,
                                         cudaStream_t stream);
 int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t num_groups,
                            int32_t max_group_size, int sms);
