@@ -51,9 +51,12 @@ __device__ __forceinline__ uint32_t cluster_size()
     return r;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // A word of CTA `rank`'s shared memory, at this CTA's address of it.
@@ -89,7 +92,7 @@ __device__ __forceinline__ Budget budget_of(const EvictParams& p, int s)
 
 // ONE: the CTA's part of the row is one tile, whose weights stay in registers.
 template <bool ONE>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p)
+__global__ void __launch_bounds__(kThreads, ONE ? 3 : 1) evict_select_kernel(const EvictParams p)
 {
     __shared__ uint32_t hist[4][256];
     __shared__ uint32_t sums[kWarps];
@@ -145,8 +148,15 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     auto competes = [&](int i) { return i >= c0 && i < c1 && i < t1; };
 
     uint32_t key[kPer];
-    if constexpr (ONE)
+    // ONE: the thread's tokens (bit e: token e) that may still be on the edge, and those
+    // above it
+    uint32_t open = 0, won = 0;
+    if constexpr (ONE) {
         load(t0, key);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            open |= (competes(t0 + tid * kPer + e) ? 1u : 0u) << e;
+    }
     // the kept weights are those with (key & mask) > edge, and `rest` of those equal
     uint32_t mask = 0, edge = 0;
     uint32_t rest = (uint32_t)(b.n - b.first - b.last);
@@ -158,13 +168,20 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     __syncthreads();
     for (int round = 0; choose && round < 4; ++round) {
         const int shift = 24 - 8 * round;
-        for (int base = t0; base < t1; base += kTile) {
-            if constexpr (!ONE)
+        if constexpr (ONE) {
+            if (open != 0)
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if ((open >> e) & 1u)
+                        atomicAdd(&hist[round][(key[e] >> shift) & 255u], 1u);
+        } else {
+            for (int base = t0; base < t1; base += kTile) {
                 load(base, key);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                if (competes(base + tid * kPer + e) && (key[e] & mask) == edge)
-                    atomicAdd(&hist[round][(key[e] >> shift) & 255u], 1u);
+                for (int e = 0; e < kPer; ++e)
+                    if (competes(base + tid * kPer + e) && (key[e] & mask) == edge)
+                        atomicAdd(&hist[round][(key[e] >> shift) & 255u], 1u);
+            }
         }
         if (size > 1)
             cluster_sync();
@@ -173,8 +190,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         // bin 255 - tid: how many lie in it and above it
         uint32_t mine = 0, incl = 0;
         if (tid < 256) {
-            for (uint32_t r = 0; r < size; ++r)
-                mine += size > 1 ? peer_word(&hist[round][255 - tid], r) : hist[round][255 - tid];
+            if (size == 1) {
+                mine = hist[round][255 - tid];
+            } else {
+                uint32_t v[kMaxCluster];       // (all on their way at once)
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxCluster; ++r)
+                    v[r] = r < size ? peer_word(&hist[round][255 - tid], r) : 0u;
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxCluster; ++r)
+                    mine += v[r];
+            }
             incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -199,20 +225,32 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         edge |= digit << shift;
         mask |= 255u << shift;
         rest -= above;
+        if (ONE && open != 0) {
+            const uint32_t d = digit;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const uint32_t x = (key[e] >> shift) & 255u;
+                const uint32_t bit = open & (1u << e);
+                won |= x > d ? bit : 0u;
+                open ^= x != d ? bit : 0u;
+            }
+        }
         if (inside == rest)                    // all that share these bits stay
             break;
     }
 
     // how many tokens of the CTA lie above, and on, the edge
     auto classify = [&](int base, uint32_t& packed, uint32_t& above_bits, uint32_t& equal_bits) {
-        above_bits = equal_bits = 0;
+        above_bits = won, equal_bits = open;
+        if constexpr (!ONE) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            if (competes(base + tid * kPer + e)) {
-                const uint32_t k = key[e] & mask;
-                above_bits |= (k > edge ? 1u : 0u) << e;
-                equal_bits |= (k == edge ? 1u : 0u) << e;
-            }
+            for (int e = 0; e < kPer; ++e)
+                if (competes(base + tid * kPer + e)) {
+                    const uint32_t k = key[e] & mask;
+                    above_bits |= (k > edge ? 1u : 0u) << e;
+                    equal_bits |= (k == edge ? 1u : 0u) << e;
+                }
+        }
         packed = __popc(above_bits) | (__popc(equal_bits) << 16);      // (a tile: 4,096 at most)
     };
     // exclusive sum over the CTA's threads; `total`: of all
@@ -253,12 +291,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         if (tid == 0)
             counts[0] = a, counts[1] = q;
         cluster_sync();
-        for (uint32_t r = 0; r < rank; ++r) {
-            n_above += peer_word(&counts[0], r);
-            n_equal += peer_word(&counts[1], r);
+        uint32_t va[kMaxCluster], vq[kMaxCluster];
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            va[r] = r < rank ? peer_word(&counts[0], r) : 0u;
+            vq[r] = r < rank ? peer_word(&counts[1], r) : 0u;
         }
-        // (nobody leaves while others may read its shared memory)
-        cluster_sync();
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r)
+            n_above += va[r], n_equal += vq[r];
+        // (nobody leaves while others may read its shared memory: the wait is at the end)
+        cluster_arrive();
     }
     for (int base = t0; base < t1; base += kTile) {
         if constexpr (!ONE)
@@ -268,31 +311,38 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         const uint32_t before = scan(packed, total);
         uint32_t above_so_far = n_above + (before & 0xffffu);
         uint32_t equal_so_far = n_equal + (before >> 16);
+        const int i0 = base + tid * kPer;
+        if (i0 < t1) {
+            float w[kPer];                     // (all on their way at once)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int i = base + tid * kPer + e;
-            if (i >= t1)
-                break;
-            int pos = -1;
-            if (i < c0) {
-                pos = i;
-            } else if (i >= c1) {
-                pos = b.n - (b.ctx - i);
-            } else {
-                const bool is_above = (ab >> e) & 1u, is_equal = (eb >> e) & 1u;
-                if (is_above || (is_equal && equal_so_far < rest))
-                    pos = c0 + (int)(above_so_far + min(equal_so_far, rest));
-                above_so_far += is_above;
-                equal_so_far += is_equal;
-            }
-            if (pos >= 0) {
-                kept[pos] = i;
-                out[pos] = __ldg(row + i);
+            for (int e = 0; e < kPer; ++e)
+                w[e] = __ldg(row + min(i0 + e, t1 - 1));
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int i = i0 + e;
+                int pos = -1;
+                if (i < c0) {
+                    pos = i;
+                } else if (i >= c1) {
+                    pos = b.n - (b.ctx - i);
+                } else {
+                    const bool is_above = (ab >> e) & 1u, is_equal = (eb >> e) & 1u;
+                    if (is_above || (is_equal && equal_so_far < rest))
+                        pos = c0 + (int)(above_so_far + min(equal_so_far, rest));
+                    above_so_far += is_above;
+                    equal_so_far += is_equal;
+                }
+                if (pos >= 0 && i < t1) {
+                    kept[pos] = i;
+                    out[pos] = w[e];
+                }
             }
         }
         n_above += total & 0xffffu;
         n_equal += total >> 16;
     }
+    if (size > 1)
+        cluster_wait();
 }
 
 // Sixteen E4M3 codes times f.
