@@ -899,14 +899,16 @@ def pkv_evict(cache, block_tables, context_lens, max_context_len, weights, keep_
     most = min(max_keep_len, max_context_len)
     at, seq, head = _totals(weights, "weights", num_seqs, kv, max_context_len, dev)
 
-    def make(fn):
-        return fn() if stream is None else _allocate(fn, stream)
-
     if weights_out is None:
-        weights_out = make(lambda: torch.empty(weights.shape, dtype=_F32, device=weights.device))
+        weights_out = torch.empty_like(weights, memory_format=torch.contiguous_format) \
+            if stream is None else \
+            _allocate(lambda: torch.empty(weights.shape, dtype=_F32, device=weights.device), stream)
+    elif weights_out is weights:
+        raise ValueError("weights_out must not be weights")
     to, to_seq, to_head = _totals(weights_out, "weights_out", num_seqs, kv, most, dev)
     if lens_out is None:
-        lens_out = make(lambda: torch.empty(num_seqs, dtype=_I32, device=weights.device))
+        lens_out = torch.empty_like(context_lens) if stream is None else \
+            _allocate(lambda: torch.empty_like(context_lens), stream)
     elif lens_out.numel() != num_seqs:
         raise ValueError("lens_out needs num_seqs entries")
     need = 0 if workspace is not None else pkv_evict_workspace_bytes(cache, num_seqs, max_keep_len,
