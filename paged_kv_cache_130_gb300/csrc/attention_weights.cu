@@ -42,6 +42,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "context_internal.h"
 #include "pkv_common.cuh"
 #include "tc_common.cuh"
@@ -594,17 +596,24 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                             const volatile float* ks = ks_ring[(tile + j) % kScaleRing];
                             // The reference only has to keep the sum from overflowing: any
                             // score of the row will do, the sum's own precision does the rest.
-                            float u = 0.f;
-                            if (!edge) {
-                                float2 ls[2] = {};
+                            float2 ls[2] = {};
+                            auto add_up = [&](auto masked) {
                                 for_columns(t_s, kRows, [&](float(&x)[16], int c0) {
+                                    if constexpr (decltype(masked)::value) {
+                                        const int lim = pos - key0 - c0;       // the last key the row sees
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e)
+                                            x[e] = e <= lim ? x[e] : kNegInf;
+                                    }
                                     float fb[2];
 #pragma unroll
                                     for (int b = 0; b < 2; ++b)
                                         fb[b] = fmaxf(E8 ? f * ks[c0 / 8 + b] : f, kTiny);
+                                    // (a row that sees any key of a tile sees its first)
                                     if (m_run == kNegInf)
                                         m_run = x[0] * fb[0];
-                                    const float2 nm2 = make_float2(-m_run, -m_run);
+                                    const float nm = decltype(masked)::value && m_run == kNegInf ? 0.f : -m_run;
+                                    const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
                                     for (int e = 0; e < 16; e += 2) {
                                         const float2 t = ffma2(make_float2(x[e], x[e + 1]),
@@ -613,9 +622,13 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                                                                  make_float2(fast_exp2(t.x), fast_exp2(t.y)));
                                     }
                                 });
-                                u = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                            }
-                            if (!__any_sync(0xffffffffu, edge || !(u < kMuch))) {
+                            };
+                            if (edge)
+                                add_up(std::true_type{});
+                            else
+                                add_up(std::false_type{});
+                            const float u = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                            if (!__any_sync(0xffffffffu, !(u < kMuch))) {
                                 l_run += u;
                             } else {
                                 for_columns(t_s, kRows, [&](float(&x)[16], int c0) {
@@ -692,9 +705,9 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                             const bool edge = (w.j0 + j) * kRows + kRows - 1 > w.first_pos;
                             // the first row that sees the key, of the q tile's
                             const int lo = (key - w.first_pos) * p.group - row0 - qt * kRows;
-                            if (!edge && end == kRows && even) {
-                                const float f = fmaxf(k_scale * info[0], kTiny);
-                                const float2 f2 = make_float2(f, f);
+                            const float f = fmaxf(k_scale * info[0], kTiny);
+                            const float2 f2 = make_float2(f, f);
+                            if (even && !edge && end == kRows) {
                                 for_columns(t_s, kRows, [&](float(&x)[16], int c0) {
                                     const float* at_l = info + kRows + c0;
 #pragma unroll
@@ -707,8 +720,31 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                                         acc[1] = fadd2(acc[1], make_float2(fast_exp2(b.x), fast_exp2(b.y)));
                                     }
                                 });
+                            } else if (even) {
+                                for_columns(t_s, end, [&](float(&x)[16], int c0) {
+                                    const float* at_l = info + kRows + c0;
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 4) {
+                                        const float4 l = *reinterpret_cast<const float4*>(at_l + e);
+                                        const float2 a = ffma2(make_float2(x[e], x[e + 1]), f2, make_float2(l.x, l.y));
+                                        const float2 b =
+                                            ffma2(make_float2(x[e + 2], x[e + 3]), f2, make_float2(l.z, l.w));
+                                        x[e] = fast_exp2(a.x), x[e + 1] = fast_exp2(a.y);
+                                        x[e + 2] = fast_exp2(b.x), x[e + 3] = fast_exp2(b.y);
+                                    }
+                                    // (a row's sum may be NaN, which keys it does not see are not)
+                                    if (edge || c0 + 16 > end) {
+                                        const int from = min(max(lo - c0, 0), 16), n = min(end - c0, 16);
+                                        const uint32_t rows = (0xffffu << from) & (0xffffu >> (16 - n));
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e)
+                                            x[e] = (rows >> e) & 1u ? x[e] : 0.f;
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2)
+                                        acc[(e >> 1) & 1] = fadd2(acc[(e >> 1) & 1], make_float2(x[e], x[e + 1]));
+                                });
                             } else {
-                                // (a row's sum may be NaN, which keys it does not see are not)
                                 for_columns(t_s, end, [&](float(&x)[16], int c0) {
                                     const float* at_f = info + c0;
 #pragma unroll
