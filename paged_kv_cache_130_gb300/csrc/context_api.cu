@@ -89,14 +89,14 @@ void place(pkv::DecodeParams& p, const Partials& w, char* ws)
     p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
 }
 
-// (behind them: units before each sequence, the tile of each)
+// (behind them: units before each group and sequence)
 Partials shared_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, int32_t num_groups,
                        int32_t max_group_size)
 {
     const int32_t members = max_group_size < num_seqs ? max_group_size : num_seqs;
     return partials(pkv::decode_prefix_rows(num_seqs, num_heads, num_heads / c->num_kv_heads, num_groups,
                                             members, device_sms()),
-                    c->head_dim, round_up(4 * (3 * (int64_t)num_seqs + 1), 256));
+                    c->head_dim, round_up(4 * ((int64_t)num_groups + num_seqs + 1), 256));
 }
 
 // The decode that adds its weights: contexts up to kOnePass tokens are one CTA's

@@ -129,12 +129,11 @@ constexpr int kMaxBalanced = 1024;         // sequences
 //     summed over the query heads of its KV head, is added to `weights`: here where
 //     a CTA holds whole contexts, else by the kernel of decode_weights.cu.
 //   kShared: sequences [grp_begin[i], grp_begin[i + 1]) share their leading blocks.
-//     An item is a tile of up to 8 or 16 rows (members of a group x query heads of
-//     a KV head): the prefix, seen by all of them, then each member's own tokens,
-//     seen by its rows.  (With prefix_partition, prefixes have a kernel of their
-//     own, and items the own tokens only.)
+//     A group's prefix is read once for each `rows` rows (members x query heads of
+//     a KV head), each sequence's own tokens for its query heads; the reduce
+//     kernel merges what belongs to a row.
 constexpr int kPlain = 0, kWeights = 1, kShared = 2;
-constexpr int kMaxEntries = kSharedEntries;        // kShared: sequences, and groups beside them
+constexpr int kMaxEntries = kSharedEntries;        // kShared: groups and sequences
 
 template <int MODE>
 constexpr int max_entries()
@@ -197,6 +196,12 @@ __device__ __forceinline__ Group group_at(const DecodeParams& p, int i, bool fla
     return g;
 }
 
+// Row tiles of a group's prefix: `rt` rows (member, query head) each.
+__device__ __forceinline__ int tiles_of(const DecodeParams& p, const Group& g, int rt)
+{
+    return ceil_div_i(g.members * p.group, rt);
+}
+
 // The group of sequence s (the last that starts at or before it).
 __device__ __forceinline__ int group_of(const DecodeParams& p, int s)
 {
@@ -223,14 +228,24 @@ __device__ __forceinline__ int own_begin(const DecodeParams& p, int s, int ctx, 
     return g.prefix;
 }
 
-// A sequence of a shared batch.
+// An entry of a shared batch: the groups' prefixes, then the sequences' own tokens.
+// The item of a KV head begins at token `from` (of sequence `from`: a prefix) and ends
+// before token `end`.
 struct Entry {
-    int pre, end;              // its own tokens [pre, end); end < 0: its output is zero
-    int first, group;          // equal for neighbours of one tile
+    int from, end;
+    int rows;                  // members x query heads of a KV head; 0: no item
 };
 
-__device__ __forceinline__ Entry entry_at(const DecodeParams& p, int s, const int* begins, int rt, bool flag)
+__device__ __forceinline__ Entry entry_at(const DecodeParams& p, int e, const int* begins, bool flag)
 {
+    Entry en{0, 0, 0};
+    if (e < p.num_groups) {
+        const Group g = group_at(p, e, flag);
+        if (g.prefix > 0 && p.prefix_partition == 0)
+            en = Entry{g.begin, g.prefix, g.members * p.group};
+        return en;
+    }
+    const int s = e - p.num_groups;
     const int ctx = __ldg(p.context_lens + s);
     int i = 0, hi = p.num_groups;              // the group: the last that starts at or before s
     while (hi - i > 1) {
@@ -240,77 +255,41 @@ __device__ __forceinline__ Entry entry_at(const DecodeParams& p, int s, const in
         else
             hi = mid;
     }
-    const Group g = group_at(p, i, false);
     bool bad;
-    const int pre = own_begin(p, s, ctx, i, g, bad);
+    const int pre = own_begin(p, s, ctx, i, group_at(p, i, false), bad);
     if (bad && flag)
         flag_error(p.dev_err, PKV_DEVERR_CONTEXT);
-    Entry en{pre, bad ? -1 : ctx, s, -1};
-    if (s >= g.begin && s - g.begin < g.members) {
-        const int per = max(1, rt / p.group);
-        en.first = g.begin + (s - g.begin) / per * per;
-        en.group = i;
-    }
+    if (!bad && ctx > pre)
+        en = Entry{pre, ctx, p.group};
     return en;
 }
 
-// The tile of sequence s: neighbours of one (first, group), at most rt / group.
-__device__ __forceinline__ bool same_tile(const Entry& a, const Entry& b)
+// Its units (of one KV head), with all the row tiles of a prefix.
+__device__ __forceinline__ int entry_units(const DecodeParams& p, int e, const Entry& en, int rt)
 {
-    return a.first == b.first && a.group == b.group && a.group >= 0;
-}
-
-__device__ __forceinline__ int tile_begin(const Entry* table, int s)
-{
-    while (s > 0 && same_tile(table[s - 1], table[s]))
-        --s;
-    return s;
-}
-
-__device__ __forceinline__ int tile_end(const Entry* table, int s, int num_seqs)
-{
-    do
-        ++s;
-    while (s < num_seqs && same_tile(table[s - 1], table[s]));
-    return s;
-}
-
-// Units of sequence s (of one KV head); a tile's first has those of the prefix and of
-// starting an item, the others' own tokens one more for the change of table.
-__device__ __forceinline__ int entry_units(const DecodeParams& p, int s, const Entry* table)
-{
-    const Entry en = table[s];
-    const int own = en.end > en.pre ? ceil_div_i(en.end - en.pre, kUnit) : 0;
-    if (s > 0 && same_tile(table[s - 1], en))
-        return own > 0 ? own + 1 : 0;
-    const int end = tile_end(table, s, p.num_seqs);
-    int pre = 0, tokens = own;
-    for (int k = s; k < end; ++k)
-        if (table[k].end >= 0) {
-            pre = p.prefix_partition == 0 ? table[k].pre : 0;
-            tokens += table[k].end - table[k].pre;
-        }
-    if (tokens + pre == 0)
+    if (en.rows == 0)
         return 0;
-    return kItemUnits + (pre > 0 ? ceil_div_i(pre, kUnit) + 1 : 0) + (own > 0 ? own + 1 : 0);
+    return e < p.num_groups ? (ceil_div_i(en.end, kUnit) + kItemUnits) * ceil_div_i(en.rows, rt)
+                            : ceil_div_i(en.end - en.from, kUnit) + kItemUnits;
 }
 
-// Shared memory of a shared batch beside the kernel's own: its sequences, and the
+// Shared memory of a shared batch beside the kernel's own: its entries, and the
 // groups' first members.
 inline size_t shared_entries_bytes(int num_groups, int num_seqs)
 {
-    return (size_t)num_seqs * sizeof(Entry) + ((size_t)num_groups + 1) * sizeof(int);
+    return ((size_t)num_groups + num_seqs) * sizeof(Entry) + ((size_t)num_groups + 1) * sizeof(int);
 }
 
-// first[s] = units before sequence s (of one KV head), first[num_seqs] = all.
-// Called by a whole CTA of kWarps warps.  Every thread takes a run of up to
-// max_entries / (32 kWarps) sequences, so that the lengths cost one round trip.
+// first[e] = units before entry e (of one KV head), first[entries] = all; an
+// entry is a sequence, or (kShared) as above.  Called by a whole CTA of kWarps
+// warps.  Every thread takes a run of up to max_entries / (32 kWarps) entries, so
+// that the lengths cost one round trip.
 template <int MODE>
 __device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, int rt, bool flag,
                                            Entry* table = nullptr)
 {
     constexpr int kRun = max_entries<MODE>() / (32 * kWarps);
-    const int entries = p.num_seqs;
+    const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
     __shared__ int sums[kWarps];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -318,25 +297,24 @@ __device__ __forceinline__ void scan_units(const DecodeParams& p, int* first, in
     const int s0 = threadIdx.x * per;
     int v[kRun];
     int sum = 0;
+    int* begins = reinterpret_cast<int*>(table + entries);
     if constexpr (MODE == kShared) {
-        int* begins = reinterpret_cast<int*>(table + entries);
-        for (int i = threadIdx.x; i <= p.num_groups; i += 32 * kWarps) {
+        for (int i = threadIdx.x; i <= p.num_groups; i += 32 * kWarps)
             begins[i] = __ldg(p.grp_begin + i);
-            if (flag && i < p.num_groups)
-                group_at(p, i, true);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-            if (i < per && s0 + i < entries)
-                table[s0 + i] = entry_at(p, s0 + i, begins, rt, flag);
         __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
         v[i] = 0;
-        if (i < per && s0 + i < entries)
-            v[i] = MODE == kShared ? entry_units(p, s0 + i, table) : units_of(p, s0 + i, flag);
+        if (i < per && s0 + i < entries) {
+            if constexpr (MODE == kShared) {
+                const Entry en = entry_at(p, s0 + i, begins, flag);
+                table[s0 + i] = en;
+                v[i] = entry_units(p, s0 + i, en, rt);
+            } else {
+                v[i] = units_of(p, s0 + i, flag);
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < kRun; ++i)
@@ -440,23 +418,24 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     pdl_launch_dependents();
 
     // BAL: units left of the CTA's share, and where it stands: unit u0 of KV
-    // head bal_h of sequence bal_s (kShared: of the tile from bal_s to bal_e)
+    // head bal_h of sequence bal_s (kShared: item bal_h, head by head, of entry
+    // bal_s, whose heads have `tiles` items of n units each)
     int64_t left = 1;
     int bal_s = 0, bal_h = 0, u0 = 0;
-    [[maybe_unused]] int bal_e = 0;
+    [[maybe_unused]] int tiles = 1, bal_n = 0;
     extern __shared__ int sm_dyn[];
     [[maybe_unused]] Entry* table_e = reinterpret_cast<Entry*>(sm_dyn);    // kShared
+    [[maybe_unused]] auto enter = [&](int e) {
+        tiles = e < p.num_groups ? ceil_div_i(table_e[e].rows, RT) : 1;
+        bal_n = (sm_first[e + 1] - sm_first[e]) / tiles;
+    };
     if constexpr (BAL) {
+        const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
         scan_units<MODE>(p, sm_first, RT, blockIdx.x == 0, table_e);
         if (MODE == kShared && blockIdx.x == 0)        // for the kernel behind
-            for (int i = threadIdx.x; i <= p.num_seqs; i += kWarps * 32) {
+            for (int i = threadIdx.x; i <= entries; i += kWarps * 32)
                 x_.first[i] = sm_first[i];
-                if (i < p.num_seqs) {
-                    x_.first[p.num_seqs + 1 + 2 * i] = tile_begin(table_e, i);
-                    x_.first[p.num_seqs + 2 + 2 * i] = tile_end(table_e, i, p.num_seqs);
-                }
-            }
-        const Shares sh = shares_of(p, sm_first[p.num_seqs], gridDim.x);
+        const Shares sh = shares_of(p, sm_first[entries], gridDim.x);
         if (blockIdx.x >= sh.ctas) {
             if (beside)
                 pdl_wait_primary();
@@ -464,7 +443,7 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
         }
         const int64_t at = sh.begin(blockIdx.x);
         left = sh.begin(blockIdx.x + 1) - at;
-        int hi = p.num_seqs;                   // the last s with first[s] Hkv <= at
+        int hi = entries;                      // the last s with first[s] Hkv <= at
         while (hi - bal_s > 1) {
             const int mid = (bal_s + hi) >> 1;
             if ((int64_t)sm_first[mid] * p.num_kv_heads <= at)
@@ -472,11 +451,11 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
             else
                 hi = mid;
         }
+        int n = sm_first[bal_s + 1] - sm_first[bal_s];
         if constexpr (MODE == kShared) {
-            bal_s = tile_begin(table_e, bal_s);
-            bal_e = tile_end(table_e, bal_s, p.num_seqs);
+            enter(bal_s);
+            n = bal_n;
         }
-        const int n = sm_first[MODE == kShared ? bal_e : bal_s + 1] - sm_first[bal_s];
         const int64_t in = at - (int64_t)sm_first[bal_s] * p.num_kv_heads;
         bal_h = in <= 0xffffffffll ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
         u0 = (int)(in - (int64_t)bal_h * n);
@@ -486,38 +465,46 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     bool direct;
     int64_t prow;                              // first row of the partial
     int nrows = G;
-    // kShared: the tile's sequences end at s_end; units [w0, w1) of the item are the CTA's
-    [[maybe_unused]] int s_end = 0, w0 = 0, w1 = 0, tile_pre = 0;
+    // kShared: row r is query head head G + (rr0 + r) % G of sequence s + (rr0 + r) / G
+    [[maybe_unused]] int rr0 = 0;
     [[maybe_unused]] bool whole = false;       // filed by sequence and head
     if constexpr (MODE == kShared) {
-        s = bal_s;
-        t_begin = t_end = 0;                   // (set part by part)
-        s_end = bal_e;
-        head = bal_h;
-        const int n = sm_first[s_end] - sm_first[s];
-        w0 = u0;
-        w1 = (int)min((int64_t)n, u0 + left);
-        nrows = (s_end - s) * G;
-        for (int k = s; k < s_end; ++k)
-            if (table_e[k].end >= 0)
-                tile_pre = table_e[k].pre;
-        whole = w0 <= kItemUnits && w1 == n;
-        direct = whole && (tile_pre == 0 || !beside);
-        // pieces lie behind one another, two a CTA; behind them the rows of whole
-        // items whose prefix is elsewhere, as in q
-        prow = whole ? 2 * (int64_t)gridDim.x * RT : (2 * (int64_t)blockIdx.x + (w0 <= kItemUnits ? 1 : 0)) * RT;
-        if (beside)
-            tile_pre = 0;
-        left -= w1 - w0;
-        u0 = 0;
-        if (++bal_h == p.num_kv_heads && left > 0) {
-            bal_h = 0;
-            do {
-                bal_s = bal_e;
-                bal_e = tile_end(table_e, bal_s, p.num_seqs);
-            } while (sm_first[bal_e] == sm_first[bal_s]);
+        const int e = bal_s;
+        const int n = bal_n;
+        const int u1 = (int)min((int64_t)n, u0 + left);
+        const int b = max(u0 - kItemUnits, 0) * kUnit;
+        head = bal_h / tiles;
+        const Entry en = table_e[e];
+        const int end = en.end;
+        bool prefix = e < p.num_groups;
+        if (prefix) {
+            rr0 = (bal_h - head * tiles) * RT;
+            s = en.from;
+            nrows = min(RT, en.rows - rr0);
+            t_begin = b;
+        } else {
+            s = e - p.num_groups;
+            t_begin = en.from + b;
+            prefix = en.from > 0;
         }
-        if (w1 <= kItemUnits)
+        t_end = min(end, t_begin - b + (u1 - kItemUnits) * kUnit);
+        whole = u0 <= kItemUnits && u1 == n;
+        direct = whole && !prefix;
+        // pieces lie behind one another, two a CTA; behind them the rows of whole
+        // items: the own tokens' as in q, then the prefixes'
+        prow = whole ? 2 * (int64_t)gridDim.x * RT +
+                           (e < p.num_groups ? (int64_t)p.num_seqs * p.num_heads : 0)
+                     : (2 * (int64_t)blockIdx.x + (u0 <= kItemUnits ? 1 : 0)) * RT;
+        left -= u1 - u0;
+        u0 = 0;
+        if (++bal_h == p.num_kv_heads * tiles && left > 0) {
+            bal_h = 0;
+            do
+                ++bal_s;
+            while (sm_first[bal_s + 1] == sm_first[bal_s]);
+            enter(bal_s);
+        }
+        if (u1 <= kItemUnits)
             break;                             // the share ends before the item's tokens
     } else if constexpr (BAL) {
         s = bal_s;
@@ -561,8 +548,8 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
     // row r of the item as a row of q and out
     auto row_of = [&](int r) -> int64_t {
         if constexpr (MODE == kShared) {
-            const int m = r / G;
-            return (int64_t)(s + m) * p.num_heads + head * G + (r - m * G);
+            const int m = (rr0 + r) / G;
+            return (int64_t)(s + m) * p.num_heads + head * G + (rr0 + r - m * G);
         } else {
             return (int64_t)s * p.num_heads + head * G + r;
         }
@@ -611,8 +598,8 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
             qk[n][h] = p.qk_scale_log2 * sm_q[8 * n + 2 * t + h];
 
     const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + t_begin / BS;
-    int nblk = ceil_div_i(t_end - t_begin, BS);
-    int nstep = ceil_div_i(t_end - t_begin, 16);
+    const int nblk = ceil_div_i(t_end - t_begin, BS);
+    const int nstep = ceil_div_i(t_end - t_begin, 16);
     const int64_t tile = (int64_t)BS * D;
     const char* kbase = reinterpret_cast<const char*>(p.k_cache) + head * tile;
     const char* vbase = reinterpret_cast<const char*>(p.v_cache) + head * tile;
@@ -632,8 +619,7 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
 
     // The warp's steps are warp, warp + kWarps, ...; lane i keeps the block
     // entries and scales of step (chunk * (32 / BPS) + i / BPS).
-    int my_steps = nstep > warp ? ceil_div_i(nstep - warp, kWarps) : 0;
-    [[maybe_unused]] uint32_t seen = 0;        // kShared: bit 2 n + h: row 8 n + 2 t + h sees the tokens
+    const int my_steps = nstep > warp ? ceil_div_i(nstep - warp, kWarps) : 0;
     constexpr int SPC = 32 / BPS;              // steps whose entries the lanes hold
     int ent = -1;
     float2 ent_s = make_float2(0.f, 0.f);
@@ -732,10 +718,6 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
                 x[n][e] = (sc[n][0][e] + sc[n][1][e]) * (qk[n][e & 1] * me.ks[b]);
                 if (!me.ok[b] || (tail && tb + g + 8 * (e >> 1) >= t_end))
                     x[n][e] = kNegInf;
-                // (a test of its own: as one with those above it cost the plain decode 3 %)
-                if constexpr (MODE == kShared)
-                    if (!((seen >> (2 * n + (e & 1))) & 1u))
-                        x[n][e] = kNegInf;
                 raise |= x[n][e] > m_h[n][e & 1] + kRaise;
             }
         if constexpr (MODE == kWeights) {
@@ -824,62 +806,16 @@ __global__ void __launch_bounds__(kWarps * 32, NNT == 1 ? 3 : 2)
 
     Step<D> sa, sb;
     Meta ma, mb;
-    if constexpr (MODE != kShared) {
-        if (my_steps > 0)
-            load(0, sa, ma);
-        for (int it = 0; it < my_steps; it += 2) {
-            if (it + 1 < my_steps)
-                load(it + 1, sb, mb);
-            compute(it, sa, ma);
-            if (it + 1 < my_steps) {
-                if (it + 2 < my_steps)
-                    load(it + 2, sa, ma);
-                compute(it + 1, sb, mb);
-            }
-        }
-    } else {
-        // the prefix (k = s - 1), then each member's own tokens
-        int off = kItemUnits;                  // units before the part
-#pragma unroll 1
-        for (int k = tile_pre > 0 ? s - 1 : s; k < s_end; ++k) {
-            int from = 0, end = tile_pre, row = k;
-            if (k >= s) {
-                from = table_e[k].pre;
-                end = table_e[k].end;
-            }
-            if (end <= from)
-                continue;
-            const int len = ceil_div_i(end - from, kUnit);
-            const int a = max(w0, off + 1), b = min(w1, off + 1 + len);
-            if (a < b) {
-                if (k < s)
-                    row = __ldg(p.grp_begin + table_e[s].group);
-                t_begin = from + (a - off - 1) * kUnit;
-                t_end = min(end, from + (b - off - 1) * kUnit);
-                table = p.block_tables + (int64_t)row * p.max_blocks_per_seq + t_begin / BS;
-                nblk = ceil_div_i(t_end - t_begin, BS);
-                nstep = ceil_div_i(t_end - t_begin, 16);
-                my_steps = nstep > warp ? ceil_div_i(nstep - warp, kWarps) : 0;
-                seen = 0;
-#pragma unroll
-                for (int i = 0; i < 2 * NNT; ++i) {
-                    const int m = s + (8 * (i >> 1) + 2 * t + (i & 1)) / G;
-                    seen |= (k >= s ? m == k : m < s_end && table_e[m].end >= 0) ? 1u << i : 0u;
-                }
-                if (my_steps > 0)
-                    load(0, sa, ma);
-                for (int it = 0; it < my_steps; it += 2) {
-                    if (it + 1 < my_steps)
-                        load(it + 1, sb, mb);
-                    compute(it, sa, ma);
-                    if (it + 1 < my_steps) {
-                        if (it + 2 < my_steps)
-                            load(it + 2, sa, ma);
-                        compute(it + 1, sb, mb);
-                    }
-                }
-            }
-            off += len + 1;
+    if (my_steps > 0)
+        load(0, sa, ma);
+    for (int it = 0; it < my_steps; it += 2) {
+        if (it + 1 < my_steps)
+            load(it + 1, sb, mb);
+        compute(it, sa, ma);
+        if (it + 1 < my_steps) {
+            if (it + 2 < my_steps)
+                load(it + 2, sa, ma);
+            compute(it + 1, sb, mb);
         }
     }
 
@@ -1001,6 +937,7 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         first = x_.first;                      // (filed by the kernel before)
     else
         scan_units<MODE>(p, sm_first, rows_per_partial, false);
+    const int entries = MODE == kShared ? p.num_groups + p.num_seqs : p.num_seqs;
     const int lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
     const int64_t row = (int64_t)blockIdx.x * kReduceRows + (threadIdx.x >> 5);
@@ -1010,8 +947,11 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     const int hq = (int)(row - (int64_t)s * p.num_heads);
     const int head = hq / p.group;
     int r = hq - head * p.group;
+    const int e = MODE == kShared ? p.num_groups + s : s;
+    // kShared: the prefix's item (item number ipre of group gpre), if the row has one
+    [[maybe_unused]] int npre = 0, rpre = 0, gpre = 0;
+    [[maybe_unused]] int64_t ipre = 0;
     bool zero = false;
-    [[maybe_unused]] int npre = 0;             // kShared: runs of the prefix, with a kernel of their own
     if constexpr (MODE == kShared) {
         const int ctx = __ldg(p.context_lens + s);
         const int i = group_of(p, s);
@@ -1020,7 +960,13 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         const int pre = own_begin(p, s, ctx, i, g, bad);
         zero = bad || ctx == 0;
         if (!bad && pre > 0) {
-            npre = p.prefix_partition > 0 ? ceil_div_i(pre, p.prefix_partition) : 0;
+            const int tiles = tiles_of(p, g, rows_per_partial);
+            const int rr = (s - g.begin) * p.group + r;
+            npre = p.prefix_partition > 0 ? ceil_div_i(pre, p.prefix_partition)
+                                          : ceil_div_i(pre, kUnit) + kItemUnits;
+            rpre = rr % rows_per_partial;
+            gpre = i;
+            ipre = (int64_t)head * tiles + rr / rows_per_partial;
             // a table that differs inside the prefix: the first member's is used
             if (hq == 0 && p.dev_err != nullptr) {
                 const int32_t* a = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
@@ -1038,15 +984,8 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     float L = 0.f;
     pdl_wait_primary();
     pdl_launch_dependents();
-    // the item: of the sequence, or (kShared) of its tile
-    int s0 = s, s1 = s + 1;
-    if constexpr (MODE == kShared) {
-        s0 = first[p.num_seqs + 1 + 2 * s];
-        s1 = first[p.num_seqs + 2 + 2 * s];
-        r += (s - s0) * p.group;
-    }
-    const int n = first[s1] - first[s0];
-    const Shares sh = shares_of(p, first[p.num_seqs], grid);
+    const int n = first[e + 1] - first[e];
+    const Shares sh = shares_of(p, first[entries], grid);
     if constexpr (MODE != kShared)
         zero = n == 0;
     auto add = [&](int64_t pr, float M) {
@@ -1063,39 +1002,56 @@ __global__ void __launch_bounds__(kReduceRows * 32)
         }
     };
     if (!zero) {
-        Pieces own{0, 0};
+        Pieces own{0, 0}, pre{0, 0};
         const bool has_own = n > 0;
         if (has_own)
-            own = pieces_of(sh, (int64_t)first[s0] * p.num_kv_heads + (int64_t)head * n, n);
-        if (npre == 0 && has_own && own.c0 == own.c1)
+            own = pieces_of(sh, (int64_t)first[e] * p.num_kv_heads + (int64_t)head * n, n);
+        // (prefixes with a kernel of their own: npre runs, each with its rows)
+        const bool runs = MODE == kShared && p.prefix_partition > 0;
+        if (npre > 0 && !runs)
+            pre = pieces_of(sh, (int64_t)first[gpre] * p.num_kv_heads + ipre * npre, npre);
+        if (npre == 0 && own.c0 == own.c1)
             return;
-        // behind the pieces: rows of whole items, then those of every run of the prefixes
+        // rows of whole items: behind the pieces
         const int64_t wown = 2 * grid * rows_per_partial + row;
         const int64_t wpre = wown + rows;
         float M = kNegInf;
-        for (int i = lane; i < npre; i += 32)
-            M = fmaxf(M, p.ws_m[wpre + i * rows]);
-        if (has_own) {
-            if (own.c0 == own.c1)
-                M = fmaxf(M, p.ws_m[wown]);
-            else
-                for (uint32_t c = own.c0 + lane; c <= own.c1; c += 32)
-                    M = fmaxf(M, p.ws_m[own.row(c, rows_per_partial, r)]);
-        }
+        auto most = [&](const Pieces& pc, int rr, int64_t whole) {
+            if (pc.c0 == pc.c1) {
+                M = fmaxf(M, p.ws_m[whole]);
+                return;
+            }
+            for (uint32_t c = pc.c0 + lane; c <= pc.c1; c += 32)
+                M = fmaxf(M, p.ws_m[pc.row(c, rows_per_partial, rr)]);
+        };
+        auto sum = [&](const Pieces& pc, int rr, int64_t whole) {
+            if (pc.c0 == pc.c1) {
+                add(whole, M);
+                return;
+            }
+#pragma unroll 4
+            for (uint32_t c = pc.c0; c <= pc.c1; ++c)
+                add(pc.row(c, rows_per_partial, rr), M);
+        };
+        if (runs)
+            for (int i = lane; i < npre; i += 32)
+                M = fmaxf(M, p.ws_m[wpre + i * rows]);
+        else if (npre > 0)
+            most(pre, rpre, wpre);
+        if (has_own)
+            most(own, r, wown);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (runs) {
 #pragma unroll 4
-        for (int i = 0; i < npre; ++i)
-            add(wpre + i * rows, M);
-        if (has_own) {
-            if (own.c0 == own.c1)
-                add(wown, M);
-            else
-#pragma unroll 4
-                for (uint32_t c = own.c0; c <= own.c1; ++c)
-                    add(own.row(c, rows_per_partial, r), M);
+            for (int i = 0; i < npre; ++i)
+                add(wpre + i * rows, M);
+        } else if (npre > 0) {
+            sum(pre, rpre, wpre);
         }
+        if (has_own)
+            sum(own, r, wown);
         if constexpr (MODE == kWeights)
             if (lane == 0)
                 x_.whole[row] = make_float2(M, L == 0.f ? 0.f : 1.f / L);

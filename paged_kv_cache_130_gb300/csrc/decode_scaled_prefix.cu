@@ -1,12 +1,13 @@
 // decode_scaled_prefix.cu -- decode over a scaled cache for groups of sequences that
 // share their leading blocks.
 //
-// Few rows to a group (members x query heads of a KV head): equal shares of tiles of
-// up to 8 or 16 rows (decode_scaled_kernel.cuh): the prefix once for all of them,
-// then each member's own tokens, in one softmax.  Many rows: the prefixes go to the
-// tensor-memory kernel of prefill_scaled_kernel.cuh, 256 rows a CTA and the keys in
-// runs, beside which the shares hold the own tokens only.  The reduce merges what
-// belongs to a row.
+// Attention over [0, c) splits at the end P of the shared prefix.  Few rows (members
+// x query heads of a KV head): both parts are items of the equal shares of
+// decode_scaled_kernel.cuh: a prefix for every 8 or 16 rows of its group, read for
+// all of them at once, and each sequence's tokens from P on.  Many rows: the
+// prefixes go to the tensor-memory kernel of prefill_scaled_kernel.cuh, 256 rows a
+// CTA and the keys in runs, beside which the shares hold the own tokens only.  The
+// reduce merges what belongs to a row.
 #include <cuda_runtime.h>
 
 #include "decode_scaled_kernel.cuh"
@@ -126,7 +127,7 @@ cudaError_t run(const DecodeParams& p0, const float* scales, int32_t* first, int
         return cudaErrorInvalidDevice;
     if (!configured[dev]) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)shared_entries_bytes(0, kSharedEntries));
+                                 (int)shared_entries_bytes(kSharedEntries, 1));
         if (e != cudaSuccess)
             return e;
         configured[dev] = true;
@@ -179,14 +180,14 @@ cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scal
 }
 
 // Two pieces a CTA, the rows of sequences whose own tokens one CTA held, those of the
-// prefixes' runs.
+// prefixes: of what one CTA held, or of every run.
 int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t num_groups,
                            int32_t max_group_size, int sms)
 {
     const int rt = rows_of(group, max_group_size);
     const int64_t runs = many_rows(group, max_group_size)
                              ? most_runs(num_groups, num_heads / group, group, max_group_size, sms)
-                             : 0;
+                             : 1;
     return 2 * decode_scaled_ctas(rt, sms) * rt + (1 + runs) * (int64_t)num_seqs * num_heads;
 }
 

@@ -68,7 +68,7 @@ struct DecodeExtra {
     int64_t weights_seq;           // elements between sequences, KV heads
     int64_t weights_head;
     float2* whole;                 // [num_seqs][num_heads]: (maximum, 1 / sum) of items one CTA held
-    int32_t* first;                // shared prefixes: units before each sequence, the tile of each
+    int32_t* first;                // shared prefixes: units before each group and sequence
 };
 
 constexpr int kWeightsSeqs = 1024;     // sequences a launch takes
@@ -79,8 +79,8 @@ cudaError_t launch_decode_weights(const DecodeParams& p, const float* scales, co
                                   int sms, cudaStream_t stream);
 
 // Shared prefixes (p.grp_*): ws_m, ws_l, ws_o of decode_prefix_rows rows, `first` of
-// 3 num_seqs + 1 entries.
-constexpr int kSharedEntries = 2048;   // groups and sequences a launch takes, together
+// one more entry than groups and sequences.
+constexpr int kSharedEntries = 2048;   // groups and sequences a launch takes
 cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scales, int32_t* first, int sms,
                                         cudaStream_t stream);
 int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t num_groups,
