@@ -982,12 +982,19 @@ __global__ void __launch_bounds__(kReduceRows * 32)
     for (int d = 0; d < DPL; ++d)
         acc[d] = 0.f;
     float L = 0.f;
+    int n = 0;
+    Shares sh;
+    if constexpr (MODE != kShared) {
+        n = first[e + 1] - first[e];
+        sh = shares_of(p, first[entries], grid);
+        zero = n == 0;
+    }
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int n = first[e + 1] - first[e];
-    const Shares sh = shares_of(p, first[entries], grid);
-    if constexpr (MODE != kShared)
-        zero = n == 0;
+    if constexpr (MODE == kShared) {
+        n = first[e + 1] - first[e];
+        sh = shares_of(p, first[entries], grid);
+    }
     auto add = [&](int64_t pr, float M) {
         const float m = p.ws_m[pr];
         const float f = m == kNegInf ? 0.f : exp2_fast(m - M);

@@ -162,6 +162,28 @@ def test_shared_prefix_without_prefixes_is_the_decode():
     assert int(b.err.item()) == 0
 
 
+@pytest.mark.parametrize("heads,kv,d,members", [(2, 2, 64, 3), (4, 1, 128, 2), (3, 1, 128, 20)])
+def test_shared_prefix_nan_reaches_who_sees_it(heads, kv, d, members):
+    """A NaN among a member's own values makes that member's output NaN in its column,
+    one of the prefix everybody's, and no other."""
+    b = Shared(735, W.F16, heads, kv, d, 16, [(4, [70] * members), (0, [50])])
+    ref = b.attention(0.125)
+    own, common = int(b.tables[1, 5]), int(b.tables[0, 2])
+    b.k[common, 0, 3, 7] = 0x40                      # (an ordinary key beside it)
+    for pool in (b.v, b.gv):
+        pool[own, 0, 9, 11] = 0x7f
+        pool[common, 0, 3, 40] = 0xff
+    b.gk[common, 0, 3, 7] = 0x40
+    ref = b.attention(0.125)
+    nan = np.isnan(ref)
+    g = heads // kv
+    assert nan[1, :g, 11].all() and nan[:members, :g, 40].all() and nan.sum() == g * (members + 1)
+    out = b.shared(0.125).double().cpu().numpy()
+    assert np.array_equal(np.isnan(out), nan)
+    H.assert_attention_close(np.nan_to_num(out), np.nan_to_num(ref), "others", W.F16)
+    assert int(b.err.item()) == 0
+
+
 def zero_rows(out, rows):
     return bool((out[rows] == 0).all())
 
