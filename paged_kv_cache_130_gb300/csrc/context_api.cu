@@ -28,10 +28,10 @@ bool sizes_known(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, i
            max_context_len <= INT_MAX - 1024;
 }
 
-// Rows of at least `len` entries that do not overlap.
+// Rows of at least `len` entries that do not overlap (null where there are none).
 bool weights_ok(const float* w, int64_t seq, int64_t head, int32_t num_seqs, int32_t heads, int64_t len)
 {
-    return w != nullptr && aligned(w, 4) && (heads <= 1 || head >= len) &&
+    return (w != nullptr || len == 0) && aligned(w, 4) && (heads <= 1 || head >= len) &&
            (num_seqs <= 1 || seq >= (heads - 1) * head + len);
 }
 
@@ -410,7 +410,7 @@ pkv_status pkv_evict(const pkv_cache_desc* cache, float* scales, int32_t num_seq
         !weights_ok(weights, weights_seq, weights_head, num_seqs, cache->num_kv_heads, max_context_len) ||
         !weights_ok(weights_out, weights_out_seq, weights_out_head, num_seqs, cache->num_kv_heads,
                     weights_out_len) ||
-        weights == weights_out)
+        (weights == weights_out && weights != nullptr))
         return PKV_ERR_INVALID_ARG;
     const int64_t need = 4 * (int64_t)num_seqs * cache->num_kv_heads * most;
     if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || (int64_t)workspace_bytes < need))

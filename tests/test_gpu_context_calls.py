@@ -282,3 +282,15 @@ def test_evict_of_many_sequences():
     e = Evicted(421, torch.float16, 64, 8, 1, r.integers(0, 60, 700), r.integers(0, 40, 700), 2, 3)
     e.check(*e.run())
     assert int(e.err.item()) == 0
+
+
+def test_evict_of_empty_contexts():
+    """No context has a token: lengths of zero, rows of zeros, or no rows at all."""
+    e = Evicted(422, "scaled", 64, 16, 2, [0, 0], [5, 0], 1, 1)
+    lens, out = e.run()
+    assert lens.tolist() == [0, 0] and not out.any() and int(e.err.item()) == 0
+    none = torch.zeros(2, 2, 0, device="cuda")
+    lens, out = B.pkv_evict(B.cache_desc(e.gk, e.gv), e.dev(e.tables), e.dev(e.ctx), 0, none,
+                            e.dev(e.keep), 5, 1, 1, e.dev(e.dst), scales=e.gs, dev_err=e.err)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [0, 0] and out.shape == (2, 2, 0) and int(e.err.item()) == 0
