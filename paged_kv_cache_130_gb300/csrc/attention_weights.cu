@@ -34,10 +34,15 @@
 // Bound by the chain product - softmax - product through tensor memory, of which
 // two sets of 128 x 256 scores fit: ~2,600 cycles a key tile for 1,024 of products.
 // Measured: 32 rows of 4 prompts after 16,384..32,768 tokens (64 heads over 8, D
-// 128) 166 us; 64 rows of 8 prompts of 512..2,048 (32 heads, bf16 cache) 59 us.  On the
+// 128) 165 us; 64 rows of 8 prompts of 512..2,048 (32 heads, bf16 cache) 57 us.  On the
 // way: a CTA per run of keys with two groups of softmax warps 267 us, equal shares
 // with codes through registers 315, by bulk copies 223, both q tiles' groups side by
 // side 190, sums against any score and log sums 175, 256 rows in one product 166.
+// Block ids asked for four tiles ahead instead of two: 169 and 55.6.  Few rows (5 of 6
+// prompts of 10,594..21,189 tokens, 16 heads each its own) take 160 us at 32 tokens a
+// block and 220 at 8: ~1,700 and ~2,400 cycles a tile, one bulk copy for each block of
+// it (two teams of converting warps changed nothing).  The merge fetches 8 log sums of a row at once: one by one the sums pass over 5 prompts
+// of 8,765..17,530 tokens of one head took 31 us instead of 20.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -71,6 +76,7 @@ constexpr int kScaleRing = 16;
 constexpr float kRaise = 8.f;          // log2: how far a score may pass the running maximum
 constexpr float kMuch = 1.2676506e30f; // 2^100: sums up to here need no other reference
 constexpr int kInfo = 2 * kRows + 4;   // floats of a q tile: its rows' factors, -log2 of their sums, a flag
+constexpr int kAtOnce = 8;             // log sums of a row that are fetched together
 constexpr float kTiny = 1e-38f;        // a factor of 0 would turn a masked -inf into NaN
 
 // One sequence's rows.
@@ -799,12 +805,23 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                         for (int row = tid; row < w.rows; row += kSoftmax) {
                             const float* pt = p.partials + row;
                             const int64_t per = (int64_t)p.row_tiles * kRows;
-                            float M = kNegInf, sum = 0.f;
-                            for (int64_t c = c0; c <= c1; ++c)
-                                M = fmaxf(M, __ldcg(pt + (2 * c + (c == c0 ? 1 : 0)) * per));
-                            const float ref = M == kNegInf ? 0.f : M;
-                            for (int64_t c = c0; c <= c1; ++c)
-                                sum += fast_exp2(__ldcg(pt + (2 * c + (c == c0 ? 1 : 0)) * per) - ref);
+                            float M = kNegInf, sum = 0.f, ref = 0.f;
+                            for (int64_t c = c0; c <= c1; c += kAtOnce) {
+                                float v[kAtOnce];
+#pragma unroll
+                                for (int i = 0; i < kAtOnce; ++i)
+                                    v[i] = c + i <= c1 ? __ldcg(pt + (2 * (c + i) + (c + i == c0 ? 1 : 0)) * per)
+                                                       : kNegInf;
+                                const float was = M;
+#pragma unroll
+                                for (int i = 0; i < kAtOnce; ++i)
+                                    M = fmaxf(M, v[i]);
+                                ref = M == kNegInf ? 0.f : M;
+                                sum *= fast_exp2(was - ref);
+#pragma unroll
+                                for (int i = 0; i < kAtOnce; ++i)
+                                    sum += fast_exp2(v[i] - ref);
+                            }
                             put_row(p.row_info + item * p.row_tiles * kInfo, row, log_sum(ref, sum));
                         }
                     }

@@ -9,6 +9,10 @@
 // every row's maximum and 1 / sum.
 // Scores cost 4 bytes a query head and token, written and read (K and V: 256
 // bytes a token at D = 128), the read mostly from L2; totals another 8 bytes.
+// Measured: 64 sequences of 1,024..4,096 tokens (64 heads over 8) 80 us: decode 66, reduce 6,
+// weights 10; 16 of 8,192..32,768 (32 heads of their own) 424: 402, 6, 21.  Weights
+// added in the reduce's launch, a CTA per run of tokens: 87 and 443; the next item's
+// first blocks fetched ahead: 407 instead of 375 without weights.
 #include <cuda_runtime.h>
 
 #include "decode_scaled_kernel.cuh"
