@@ -748,7 +748,7 @@ pkv_status pkv_paged_attention_decode_scaled_weights(
  * weights_out    rows of weights_out_len entries (at least min(max_keep_len,
  *                max_context_len)): the totals of what stays, zeros behind.  Not
  *                overlapping `weights`.
- * lens_out       device int32 [num_seqs]: n.
+ * lens_out       device int32 [num_seqs]: n.  Not overlapping context_lens or keep_lens.
  * workspace      pkv_evict_workspace_bytes bytes, 256-byte aligned.
  * Precondition (not checked): the destination blocks are distinct, and none is a
  * block of a sequence of the batch.

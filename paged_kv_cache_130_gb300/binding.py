@@ -911,6 +911,8 @@ def pkv_evict(cache, block_tables, context_lens, max_context_len, weights, keep_
             _allocate(lambda: torch.empty_like(context_lens), stream)
     elif lens_out.numel() != num_seqs:
         raise ValueError("lens_out needs num_seqs entries")
+    elif lens_out is context_lens or lens_out is keep_lens:
+        raise ValueError("lens_out must not be context_lens or keep_lens")
     need = 0 if workspace is not None else pkv_evict_workspace_bytes(cache, num_seqs, max_keep_len,
                                                                      max_context_len)
     workspace, wp, ws_bytes = _workspace(workspace, need, dev, stream, weights.device)

@@ -35,6 +35,13 @@ bool weights_ok(const float* w, int64_t seq, int64_t head, int32_t num_seqs, int
            (num_seqs <= 1 || seq >= (heads - 1) * head + len);
 }
 
+// Two arrays of n entries that have none in common.
+bool apart(const int32_t* a, const int32_t* b, int32_t n)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x < y ? y - x : x - y) >= sizeof(int32_t) * (uintptr_t)n;
+}
+
 pkv::DecodeParams decode_params(const pkv_cache_desc* cache, const void* q, int32_t q_dtype,
                                 int32_t num_seqs, int32_t num_heads, const int32_t* block_tables,
                                 int32_t max_blocks_per_seq, const int32_t* context_lens,
@@ -410,7 +417,8 @@ pkv_status pkv_evict(const pkv_cache_desc* cache, float* scales, int32_t num_seq
         !weights_ok(weights, weights_seq, weights_head, num_seqs, cache->num_kv_heads, max_context_len) ||
         !weights_ok(weights_out, weights_out_seq, weights_out_head, num_seqs, cache->num_kv_heads,
                     weights_out_len) ||
-        (weights == weights_out && weights != nullptr))
+        (weights == weights_out && weights != nullptr) || !apart(lens_out, context_lens, num_seqs) ||
+        !apart(lens_out, keep_lens, num_seqs))
         return PKV_ERR_INVALID_ARG;
     const int64_t need = 4 * (int64_t)num_seqs * cache->num_kv_heads * most;
     if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || (int64_t)workspace_bytes < need))

@@ -188,6 +188,13 @@ def test_evict_checks(lib, desc, kw, want):
     assert lib.pkv_evict(ctypes.byref(_desc(**desc)), *a.values()) == want
 
 
+@pytest.mark.parametrize("lens", [0x3000, 0x3004, 0x2ffc, 0x4000, 0x4004])
+def test_evict_reads_no_lengths_that_it_writes(lib, lens):
+    """lens_out over context_lens or keep_lens of two sequences."""
+    a = dict(EVICT, lens=lens)
+    assert lib.pkv_evict(ctypes.byref(_desc()), *a.values()) == INVALID
+
+
 def test_workspaces(lib):
     d = _desc()
     assert B.pkv_evict_workspace_bytes(d, 2, 100, 1000) == 2 * 8 * 100 * 4

@@ -135,6 +135,15 @@ def test_evict_refuses_its_input_as_its_output():
         fn(**dict(good, weights_out=good["weights"][:]))
 
 
+def test_evict_refuses_lengths_that_it_reads_as_its_output():
+    fn, good = arguments(200)["evict"]
+    for name in ("context_lens", "keep_lens"):
+        with pytest.raises(ValueError, match="lens_out must not be"):
+            fn(**dict(good, lens_out=good[name]))
+        with pytest.raises(B.PkvError, match="invalid"):
+            fn(**dict(good, lens_out=good[name][:]))
+
+
 def test_position_offsets_are_checked():
     b = Batch(401, W.F16, 4, 2, 64, 16, [2, 1], [3, 0])
     for bad in (i32(1), torch.zeros(2, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.int32)):
