@@ -634,14 +634,14 @@ pkv_status pkv_copy_blocks_scaled(const pkv_cache_desc* src, float* const* src_s
  * leading blocks, with the groups, bounds and device checks of
  * pkv_paged_attention_decode_shared_prefix.  Sequences are groups' members in
  * order; a shared block is read once for every 8 or 16 rows (members x query heads
- * of a KV head) of its group, where max_group_size gives more than 32 rows once for
- * every 256.  Groups without a prefix (0 blocks) and num_groups or
+ * of a KV head) of its group, where max_group_size gives more than 32 rows (16 where
+ * num_groups x num_kv_heads is 128 or more) once for every 256.  Groups without a prefix (0 blocks) and num_groups or
  * max_prefix_blocks of 0 give the plain decode.
  * Members beyond max_group_size, and members of a group whose entry cannot be
  * used, get zeros.  num_seqs + num_groups is 2,048 at most (else
  * PKV_ERR_UNSUPPORTED).  The same inputs give the same bits on one kind of GPU.
  * Calls that can overlap on the GPU need workspaces of their own.
- * Launches: two kernels, three beyond 32 rows a group.
+ * Launches: two kernels, three beyond 32 (16) rows a group.
  * ------------------------------------------------------------------------- */
 size_t pkv_decode_scaled_shared_prefix_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
                                                        int32_t num_heads, int32_t num_groups,

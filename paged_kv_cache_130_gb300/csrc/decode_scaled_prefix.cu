@@ -34,15 +34,27 @@ constexpr int kKeys = pfs::kKeys;
 //   1 of 16,384                   27 / 33  33 / 34  41 / 36  50 / 43   84 / 45
 //   8 of 2,048                    26 / 31  36 / 41  47 / 41  60 / 41  114 / 52
 //   15 of 1,024                   28 / 40  41 / 41  56 / 45  74 / 50  139 / 70
+// Where groups x KV heads keep the GPU busy anyhow, beyond half as many: 16 heads of
+// their own, rows                  16       24       32       48
+//   8 of 2,048                    60 / 65  91 / 75 105 / 84 156 / 108
+//   15 of 1,024                   90 / 90 135 / 110 162 / 129 239 / 168
+//   1 of 16,384                   35 / 50  48 / 50  48 / 51  66 / 53
 constexpr int kManyRows = 32;
+constexpr int kManyItems = 128;
 constexpr int kMinRun = 4 * kKeys;         // keys of a CTA of it
 
-bool many_rows(int32_t group, int32_t max_group_size) { return (int64_t)group * max_group_size > kManyRows; }
+bool many_rows(int32_t num_groups, int32_t num_kv_heads, int32_t group, int32_t max_group_size)
+{
+    const bool busy = (int64_t)num_groups * num_kv_heads >= kManyItems;
+    return (int64_t)group * max_group_size > (busy ? kManyRows / 2 : kManyRows);
+}
 
 // Rows of an item of the shares.
-int rows_of(int32_t group, int32_t max_group_size)
+int rows_of(int32_t num_groups, int32_t num_kv_heads, int32_t group, int32_t max_group_size)
 {
-    const int64_t rows = many_rows(group, max_group_size) ? group : (int64_t)group * max_group_size;
+    const int64_t rows = many_rows(num_groups, num_kv_heads, group, max_group_size)
+                             ? group
+                             : (int64_t)group * max_group_size;
     return group > 8 || rows > 8 ? 16 : 8;
 }
 
@@ -121,7 +133,7 @@ cudaError_t run(const DecodeParams& p0, const float* scales, int32_t* first, int
     DecodeParams p = p0;
     const int64_t ctas = decode_scaled_ctas(8 * NNT, sms);
     const int64_t rows = (int64_t)p.num_seqs * p.num_heads;
-    if (many_rows(p.group, p.max_group_size)) {
+    if (many_rows(p.num_groups, p.num_kv_heads, p.group, p.max_group_size)) {
         const int64_t n = most_runs(p.num_groups, p.num_kv_heads, p.group, p.max_group_size, sms);
         const int64_t tiles = ((int64_t)p.max_prefix_blocks * BS + kKeys - 1) / kKeys;
         const int64_t run = (tiles + n - 1) / n * kKeys;
@@ -158,8 +170,9 @@ cudaError_t run(const DecodeParams& p0, const float* scales, int32_t* first, int
 template <int QT, int D, int BS>
 cudaError_t by_rows(const DecodeParams& p, const float* scales, int32_t* first, int sms, cudaStream_t st)
 {
-    return rows_of(p.group, p.max_group_size) == 8 ? run<QT, D, BS, 1>(p, scales, first, sms, st)
-                     : run<QT, D, BS, 2>(p, scales, first, sms, st);
+    return rows_of(p.num_groups, p.num_kv_heads, p.group, p.max_group_size) == 8
+               ? run<QT, D, BS, 1>(p, scales, first, sms, st)
+               : run<QT, D, BS, 2>(p, scales, first, sms, st);
 }
 
 template <int QT, int D>
@@ -199,8 +212,8 @@ cudaError_t launch_decode_scaled_prefix(const DecodeParams& p, const float* scal
 int64_t decode_prefix_rows(int32_t num_seqs, int32_t num_heads, int32_t group, int32_t num_groups,
                            int32_t max_group_size, int sms)
 {
-    const int rt = rows_of(group, max_group_size);
-    const int64_t runs = many_rows(group, max_group_size)
+    const int rt = rows_of(num_groups, num_heads / group, group, max_group_size);
+    const int64_t runs = many_rows(num_groups, num_heads / group, group, max_group_size)
                              ? most_runs(num_groups, num_heads / group, group, max_group_size, sms)
                              : 1;
     return 2 * decode_scaled_ctas(rt, sms) * rt + (1 + runs) * (int64_t)num_seqs * num_heads;

@@ -126,6 +126,9 @@ SHARED = [
     (W.BF16, 16, 1, 128, 32, [(40, [7, 0, 0, 33, 1]), (1, [1] * 3)]),
     (W.BF16, 8, 1, 128, 8, [(200, [4] * 40), (17, [9] * 33)]),              # two CTAs' rows
     (W.F16, 3, 1, 128, 16, [(65, [2] * 90)]),
+    # more than 16, of many groups and heads
+    (W.F16, 16, 16, 64, 16, [(5, [3] * 17), (0, [9])] + [(2, [1, 20])] * 6),
+    (W.BF16, 64, 32, 128, 8, [(70, [2, 0, 33] * 5), (9, [1]), (3, [5, 1]), (1, [8] * 8)]),
 ]
 
 
