@@ -14,8 +14,8 @@
 //     its tokens come from, codes of smaller ones become E4M3(code * old / new).
 // Bound by latency for short contexts, by the gather and its writes for long ones.
 // Measured (8 heads, D 128, scaled cache): 64 contexts of 1,500..2,600 tokens to 2,048
-// 100 us: select 20, move 80, 93 % of a copy's rate; 4 of 16,384..32,768 to 2,048 28 us:
-// 17 and 9.  Three rounds of 11 bits, with larger histograms over the cluster: select 57.
+// 99 us: select 19, move 80, 93 % of a copy's rate; 4 of 16,384..32,768 to 2,048 26 us:
+// 16 and 9.  Three rounds of 11 bits, with larger histograms over the cluster: select 57.
 #include <cuda_runtime.h>
 
 #include "context_internal.h"
