@@ -261,6 +261,7 @@ WINDOWS = [
     (W.F16, 17, 1, 128, 16, [23], [1500], 23),                              # 391 rows, several runs of keys
     (W.F16, 1, 1, 64, 8, [1, 1, 1], [0, 511, 1024], 1),                     # single tokens
     (W.BF16, 128, 1, 64, 16, [4], [300], 3),
+    (W.F16, 2, 1, 64, 16, [3], [20000], 2),                                 # an item over every CTA
 ]
 
 
@@ -555,6 +556,8 @@ EVICTIONS = [
     ("e4m3", 128, 16, 2, [9000, 12], [512, 3], 2, 7),
     ("e4m3", 64, 32, 1, [64, 65, 66], [32, 33, 60], 40, 40),                 # more to keep than stays
     ("scaled", 64, 16, 1, [33000, 40000], [2049, 31000], 4, 32),             # read again in every round
+    ("scaled", 64, 16, 2, [2561, 2560, 2049], [2000, 2559, 7], 4, 32),       # CTAs between the least and the most threads
+    (torch.float16, 64, 16, 1, [4096, 4095], [1, 4000], 0, 0),
 ]
 
 
