@@ -1003,6 +1003,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                 const float v = __shfl_sync(0xffffffffu, sc, min(31, (lane * 8) >> sh));
                 if (lane < kRows / 8)
                     *const_cast<volatile float*>(&ks_ring[jj % kScaleRing][lane]) = v;
+                __syncwarp();                  // (lane 0's arrival hands on what every lane wrote)
             }
             // A block that the table does not have leaves its rows as they are (no row
             // sees them); a bad one's are zeros: filled by the tensor copy past the
