@@ -553,11 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = load(j, cur, prev);
             prev = cur;
         }
-        if (!alive) {
-            // wait (bounded) for the copies still in flight
-            for (int i = max(0, issued - ST); i < issued; ++i)
-                bar_wait(s_addr(&bars.full[i % ST]), (i / ST) & 1);
-        }
+        // the copies have landed before the CTA ends, whichever role gave up (bounded)
+        for (int i = max(0, issued - ST); i < issued; ++i)
+            bar_wait(s_addr(&bars.full[i % ST]), (i / ST) & 1);
     }
 
     tc_fence_before();
