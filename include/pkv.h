@@ -779,8 +779,8 @@ pkv_status pkv_evict(const pkv_cache_desc* cache, float* scales, int32_t num_seq
  * every such wait is bounded: after the limit it sets PKV_DEVERR_TIMEOUT in
  * dev_err, stops waiting everywhere, lets the copies it started land and
  * returns, so the context stays usable.  This call sets the number of polls
- * per wait for decode calls issued afterwards (captured into their launch
- * parameters at the call): 0 restores the kernel's own limit (2^22 polls, and
+ * per wait for decode calls, and pkv_attention_weights, issued afterwards (captured
+ * into their launch parameters at the call): 0 restores the kernel's own limit (2^22 polls, and
  * at most one second from a wait's first failed poll).  Under a lower limit a
  * poll is one look at the barrier that does not suspend the thread, so a wait
  * that is not already complete runs out.  A test sets a small value to make a

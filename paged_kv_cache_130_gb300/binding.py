@@ -316,9 +316,9 @@ def pkv_paged_attention_decode_static_ws(cache, q, block_tables, context_lens, m
 
 
 def pkv_testing_set_decode_wait_limit(tries):
-    """Polls per bounded wait of the streaming decode kernel for later decode
-    calls (0: the kernel's own limit); a testing aid.  Returns the previous
-    setting."""
+    """Polls per bounded wait of the streaming decode kernel and of attention
+    weights for later calls (0: the kernel's own limit); a testing aid.  Returns
+    the previous setting."""
     return int(load().pkv_testing_set_decode_wait_limit(int(tries)))
 
 

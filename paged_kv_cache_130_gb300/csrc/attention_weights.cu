@@ -293,44 +293,57 @@ __device__ __forceinline__ bool aborted(const int* flag)
     return *reinterpret_cast<const volatile int*>(flag) != 0;
 }
 
-__device__ __forceinline__ void set_abort(int* flag, int32_t* dev_err)
-{
-    *reinterpret_cast<volatile int*>(flag) = 1;
-    flag_error(dev_err, PKV_DEVERR_TIMEOUT);
-}
+// What every wait of a CTA shares: its flag (some role has given up), the caller's
+// error word, and the polls of a wait.  Below kSpin (a test's setting) a poll is one
+// look that does not suspend.
+struct Waits {
+    int* flag;
+    int32_t* dev_err;
+    uint32_t tries;
+
+    __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) const
+    {
+        return tries < kSpin ? test_wait(bar, parity) : try_wait(bar, parity);
+    }
+    __device__ __forceinline__ void give_up() const
+    {
+        *reinterpret_cast<volatile int*>(flag) = 1;
+        flag_error(dev_err, PKV_DEVERR_TIMEOUT);
+    }
+};
 
 // Bounded wait by one thread; gives up early once another role has aborted.
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, int* flag, int32_t* dev_err)
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const Waits& w)
 {
     WaitClock clock;
-    for (uint32_t i = 0; i < kSpin; ++i) {
-        if (try_wait(bar, parity))
+    for (uint32_t i = 0; i < w.tries; ++i) {
+        if (w.poll(bar, parity))
             return true;
-        if (aborted(flag))
+        if (aborted(w.flag))
             return false;
         if (clock.expired(i))
             break;
     }
-    set_abort(flag, dev_err);
+    w.give_up();
     return false;
 }
 
 // The same by a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* flag, int32_t* dev_err)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Waits& w)
 {
     bool ok = false;
     WaitClock clock;
-    for (uint32_t i = 0; i < kSpin; ++i) {
-        if (try_wait(bar, parity)) {
+    for (uint32_t i = 0; i < w.tries; ++i) {
+        if (w.poll(bar, parity)) {
             ok = true;
             break;
         }
-        if (aborted(flag) || clock.expired(i))
+        if (aborted(w.flag) || clock.expired(i))
             break;
     }
     ok = __all_sync(0xffffffffu, ok);
     if (!ok)
-        set_abort(flag, dev_err);
+        w.give_up();
     return ok;
 }
 
@@ -450,6 +463,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
+    const Waits waits{&abort_flag, p.dev_err, p.wait_tries ? p.wait_tries : kSpin};
 
     // what the kernel before writes is read behind the wait below; the lengths are older
     const uint32_t sb = (s_addr(smem_raw) + 1023u) & ~1023u;
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
         bool alive = true;
         uint32_t unit = 0;                             // scores this group has seen
         auto next_scores = [&]() {
-            alive = alive && wait_warp(s_addr(&bars.s_full[gi]), unit & 1, &abort_flag, p.dev_err);
+            alive = alive && wait_warp(s_addr(&bars.s_full[gi]), unit & 1, waits);
             tc_fence_after();
         };
         auto release = [&]() {
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                 const int row0 = pr * 2 * kRows;
                 for (int qt = 0; qt < nq; ++qt)
                     alive = alive && wait_warp(s_addr(&bars.q_full[(qn + qt) & 1]), ((qn + qt) >> 1) & 1,
-                                               &abort_flag, p.dev_err);
+                                               waits);
                 if constexpr (!TOTALS) {
                     // one row a thread: groups 2 x + y take tile y of two over the key
                     // tiles of parity x; of one tile every fourth key tile each
@@ -841,7 +855,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
             bool alive = true;
             auto free_group = [&](uint32_t gi) -> bool {
                 if ((used >> gi) & 1u) {
-                    if (!wait_one(s_addr(&bars.s_free[gi]), (parity >> gi) & 1u, &abort_flag, p.dev_err))
+                    if (!wait_one(s_addr(&bars.s_free[gi]), (parity >> gi) & 1u, waits))
                         return false;
                     parity ^= 1u << gi;
                 }
@@ -872,11 +886,10 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                 for (int pr = 0; alive && pr < w.pairs; ++pr) {
                     const uint32_t nq = q_tiles_of(w, pr);
                     for (uint32_t qt = 0; alive && qt < nq; ++qt)
-                        alive = wait_one(s_addr(&bars.q_full[(qn + qt) & 1]), ((qn + qt) >> 1) & 1, &abort_flag,
-                                         p.dev_err);
+                        alive = wait_one(s_addr(&bars.q_full[(qn + qt) & 1]), ((qn + qt) >> 1) & 1, waits);
                     for (int j = 0; alive && j < w.nk; ++j, ++tile) {
                         const uint32_t st = tile % ST;
-                        alive = wait_one(s_addr(&bars.full[st]), (tile / ST) & 1, &abort_flag, p.dev_err);
+                        alive = wait_one(s_addr(&bars.full[st]), (tile / ST) & 1, waits);
                         if (!alive)
                             break;
                         const uint32_t k_off = st * L::TB >> 4;
@@ -918,7 +931,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
             const int64_t at = ((int64_t)qw.s * p.num_kv_heads + qw.h) * p.row_tiles + 2 * q_pr;
             for (int qt = 0; qt < nq; ++qt, ++qn) {
                 const uint32_t slot = qn & 1;
-                if (qn >= 2 && !wait_one(s_addr(&bars.q_free[slot]), ((qn >> 1) & 1) ^ 1, &abort_flag, p.dev_err))
+                if (qn >= 2 && !wait_one(s_addr(&bars.q_free[slot]), ((qn >> 1) & 1) ^ 1, waits))
                     return false;
                 const uint32_t bar = s_addr(&bars.q_full[slot]);
                 expect_bytes(bar, L::TB + kInfo * 4);
@@ -995,7 +1008,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
             const int slot = jj % SLOTS;
             const uint32_t bar = s_addr(E8 ? &bars.raw_full[E8 ? slot : 0] : &bars.full[E8 ? 0 : slot]);
             alive = wait_warp(s_addr(E8 ? &bars.raw_free[E8 ? slot : 0] : &bars.empty[E8 ? 0 : slot]),
-                              ((jj / SLOTS) & 1) ^ 1, &abort_flag, p.dev_err);
+                              ((jj / SLOTS) & 1) ^ 1, waits);
             if (!alive)
                 break;
             if constexpr (E8) {
@@ -1044,8 +1057,8 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
             t1 = t2;
             sc = sc1;
         }
-        if (!alive && lane == 0) {
-            // what is on its way lands before the CTA ends
+        // what is on its way lands before the CTA ends, whichever role gave up (bounded)
+        if (lane == 0) {
             for (int k = max(0, jj - SLOTS); k < jj; ++k)
                 bar_wait(s_addr(E8 ? &bars.raw_full[E8 ? k % SLOTS : 0] : &bars.full[E8 ? 0 : k % SLOTS]),
                          (k / SLOTS) & 1);
@@ -1069,7 +1082,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
         const int sh = 31 - __clz(p.block_size);
         for (int jj = 0; jj < tiles; ++jj) {
             const int rs = jj % L::RAW, st = jj % ST;
-            if (!wait_warp(s_addr(&bars.raw_full[rs]), (jj / L::RAW) & 1, &abort_flag, p.dev_err))
+            if (!wait_warp(s_addr(&bars.raw_full[rs]), (jj / L::RAW) & 1, waits))
                 break;
             const uint32_t src = sb + L::raw + rs * L::RB;
             const uint32_t good = *const_cast<const volatile uint32_t*>(&raw_good[rs]);
@@ -1085,7 +1098,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
             __syncwarp();
             if (lane == 0)
                 bar_arrive(s_addr(&bars.raw_free[rs]));
-            if (!wait_warp(s_addr(&bars.empty[st]), ((jj / ST) & 1) ^ 1, &abort_flag, p.dev_err))
+            if (!wait_warp(s_addr(&bars.empty[st]), ((jj / ST) & 1) ^ 1, waits))
                 break;
             const uint32_t dst = sb + L::ring + st * L::TB;
 #pragma unroll

@@ -299,6 +299,7 @@ pkv_status pkv_attention_weights(const pkv_cache_desc* cache, const float* scale
     p.weights_seq = weights_seq;
     p.weights_head = weights_head;
     p.dev_err = dev_err;
+    p.wait_tries = pkv::decode_wait_tries();
     for (int32_t s0 = 0; s0 < num_seqs; s0 += wl.seqs) {
         p.num_seqs = num_seqs - s0 < wl.seqs ? num_seqs - s0 : wl.seqs;
         p.cu_seqlens_q = cu_seqlens_q + s0;

@@ -41,6 +41,7 @@ struct WeightsParams {
     int64_t weights_seq;
     int64_t weights_head;
     int32_t* dev_err;
+    uint32_t wait_tries;           // polls of a bounded wait; 0: the kernel's own limit
 };
 
 cudaError_t launch_attention_weights(const WeightsParams& p, cudaStream_t stream);
