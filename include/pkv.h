@@ -688,7 +688,9 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
  *                may be rounded).
  * workspace      pkv_attention_weights_workspace_bytes bytes, 256-byte aligned.
  * Device checks as for the prefill: a sequence that cannot be used gets nothing
- * added; a key of a block with a bad id is read as zeros.  The same inputs give
+ * added; a key of a block with a bad id is read as zeros.  PKV_DEVERR_TIMEOUT: where a
+ * wait for the rows' sums ran out, none of the launch's sequences gets anything added;
+ * where one ran out later, some tokens have their weights and others not.  The same inputs give
  * the same bits on one kind of GPU.
  * Launches: three kernels for every 512 sequences.  K is read twice, and again for
  * every further 256 (row, query head) rows of a KV head.
@@ -779,9 +781,10 @@ pkv_status pkv_evict(const pkv_cache_desc* cache, float* scales, int32_t num_seq
  * every such wait is bounded: after the limit it sets PKV_DEVERR_TIMEOUT in
  * dev_err, stops waiting everywhere, lets the copies it started land and
  * returns, so the context stays usable.  This call sets the number of polls
- * per wait for decode calls, and pkv_attention_weights, issued afterwards (captured
- * into their launch parameters at the call): 0 restores the kernel's own limit (2^22 polls, and
- * at most one second from a wait's first failed poll).  Under a lower limit a
+ * per wait for decode calls, and of pkv_attention_weights while it takes the rows'
+ * sums, issued afterwards (captured into their launch parameters at the call): 0
+ * restores the kernel's own limit (2^22 polls, and at most one second from a
+ * wait's first failed poll).  Under a lower limit a
  * poll is one look at the barrier that does not suspend the thread, so a wait
  * that is not already complete runs out.  A test sets a small value to make a
  * wait run out on purpose and check the error path.  Returns the previous

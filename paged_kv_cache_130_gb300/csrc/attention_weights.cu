@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles_kernel(const Weigh
     const Span sp = span_of(p, s, first && g == 0);
     if (first)
         p.finished[item] = 0;
+    if (idx == 0 && threadIdx.x == 0)
+        *p.failed = 0;
     if (tile * kRows >= sp.rows)
         return;
     const float sign = p.qk_scale_log2 < 0.f ? -1.f : (p.qk_scale_log2 == 0.f ? 0.f : 1.f);
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
-    const Waits waits{&abort_flag, p.dev_err, p.wait_tries ? p.wait_tries : kSpin};
+    const Waits waits{&abort_flag, p.dev_err, !TOTALS && p.wait_tries ? p.wait_tries : kSpin};
 
     // what the kernel before writes is read behind the wait below; the lengths are older
     const uint32_t sb = (s_addr(smem_raw) + 1023u) & ~1023u;
@@ -537,6 +539,8 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
     pdl_launch_dependents();
     if (blockIdx.x >= ctas)
         return;
+    // a wait for the sums ran out: totals stay as they are
+    const bool failed = TOTALS && __ldcg(p.failed) != 0;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
             s_addr(&tmem_holder)));
@@ -568,7 +572,9 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
         batch.enter(w);
     }
 
-    if (warp < kFetchWarp) {
+    if (failed) {
+        // ---------------- nothing to do: the CTA gives its tensor memory back ----------------
+    } else if (warp < kFetchWarp) {
         // ---------------- softmax: group gi ----------------
         const int gi = warp >> 2;
         const int r = tid & (kRows - 1);               // tensor-memory lane
@@ -1123,6 +1129,8 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
 
     tc_fence_before();
     __syncthreads();
+    if (!TOTALS && tid == 0 && aborted(&abort_flag))
+        *p.failed = 1;
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

@@ -148,7 +148,7 @@ WeightsLayout weights_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t 
 struct WindowLayout {
     int32_t seqs;              // of one launch
     int32_t row_tiles, ctas;
-    int64_t info_off, partials_off, finished_off, bytes;
+    int64_t info_off, partials_off, finished_off, failed_off, bytes;
 };
 
 WindowLayout window_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, int32_t window,
@@ -164,7 +164,8 @@ WindowLayout window_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t nu
     w.info_off = tiles * 128 * c->head_dim * 2;
     w.partials_off = round_up(w.info_off + tiles * 260 * 4, 256);
     w.finished_off = w.partials_off + 2 * (int64_t)w.ctas * w.row_tiles * 128 * 4;
-    w.bytes = w.finished_off + round_up(4 * (int64_t)w.seqs * c->num_kv_heads, 256);
+    w.failed_off = w.finished_off + 4 * (int64_t)w.seqs * c->num_kv_heads;
+    w.bytes = round_up(w.failed_off + 4, 256);
     return w;
 }
 
@@ -296,6 +297,7 @@ pkv_status pkv_attention_weights(const pkv_cache_desc* cache, const float* scale
     p.row_info = reinterpret_cast<float*>(ws + wl.info_off);
     p.partials = reinterpret_cast<float*>(ws + wl.partials_off);
     p.finished = reinterpret_cast<int32_t*>(ws + wl.finished_off);
+    p.failed = reinterpret_cast<int32_t*>(ws + wl.failed_off);
     p.weights_seq = weights_seq;
     p.weights_head = weights_head;
     p.dev_err = dev_err;

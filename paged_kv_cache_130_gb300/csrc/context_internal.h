@@ -37,11 +37,12 @@ struct WeightsParams {
     float* row_info;               // [num_seqs][num_kv_heads][row_tiles][260]: factors, -log sums, a flag
     float* partials;               // [2 ctas][row_tiles * 128]: log sums
     int32_t* finished;             // [num_seqs][num_kv_heads]: segments done
+    int32_t* failed;               // a wait of the pass for the sums ran out
     float* weights;                // element (s, h, t) at s weights_seq + h weights_head + t
     int64_t weights_seq;
     int64_t weights_head;
     int32_t* dev_err;
-    uint32_t wait_tries;           // polls of a bounded wait; 0: the kernel's own limit
+    uint32_t wait_tries;           // polls of a wait for the sums; 0: the kernel's own limit
 };
 
 cudaError_t launch_attention_weights(const WeightsParams& p, cudaStream_t stream);

@@ -65,3 +65,34 @@ def test_weights_whose_wait_runs_out_flag_it_and_the_next_call_is_right(cache, n
     assert int(b.err.item()) == 0
     add, size = OC.weights(keys, b.q, b.cu, 64, b.ctx, 0.09)
     weights_close(w, 0.0, add, size, "after a time-out")
+
+
+@pytest.mark.parametrize("cache", ["scaled", W.BF16])
+def test_weights_whose_sums_run_out_leave_the_totals_alone(cache):
+    """The limit reaches the pass for the sums only: whenever it runs out, at the first
+    wait or on the way, nothing is added; else everything is."""
+    b, kw, keys = weighed(cache, [40, 1, 300], [9000, 200, 129])
+    before = torch.rand(3, 2, b.max_ctx, device="cuda")
+    add, size = OC.weights(keys, b.q, b.cu, 64, b.ctx, 0.09)
+    ran_out = []
+    for i in range(40):
+        w = before.clone()
+        b.err.zero_()
+        B.pkv_testing_set_decode_wait_limit(int(2 ** (i / 3)))
+        try:
+            run_weights(b, 0.09, 64, w, **kw)
+            torch.cuda.synchronize()
+        finally:
+            B.pkv_testing_set_decode_wait_limit(0)
+        ran_out.append(int(b.err.item()) == B.PKV_DEVERR_TIMEOUT)
+        if ran_out[-1]:
+            assert torch.equal(w, before), i
+        else:
+            assert int(b.err.item()) == 0
+            weights_close(w, before.double().cpu().numpy()[..., :add.shape[2]], add, size, "all the same")
+    assert ran_out[0]
+    b.err.zero_()
+    w = before.clone()
+    run_weights(b, 0.09, 64, w, **kw)
+    assert int(b.err.item()) == 0
+    weights_close(w, before.double().cpu().numpy()[..., :add.shape[2]], add, size, "after a time-out")
