@@ -25,7 +25,8 @@ def weights(keys, q, cu, window, ctx, scale):
             hidden = np.arange(c)[None] > (c - n + np.arange(n))[:, None]
             x = np.where(hidden[:, None], -np.inf, x)
             p = np.exp(x - x.max(-1, keepdims=True))
-            out[s, h, :c] = (p / p.sum(-1, keepdims=True)).sum((0, 1))
+            # (a row whose sum is NaN does not reach the keys it does not see)
+            out[s, h, :c] = np.where(hidden[:, None], 0.0, p / p.sum(-1, keepdims=True)).sum((0, 1))
     return out, size
 
 

@@ -75,6 +75,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kScaleRing = 16;
 constexpr float kRaise = 8.f;          // log2: how far a score may pass the running maximum
 constexpr float kMuch = 1.2676506e30f; // 2^100: sums up to here need no other reference
+constexpr float kMost = 3.4028235e38f; // the largest float
 constexpr int kInfo = 2 * kRows + 4;   // floats of a q tile: its rows' factors, -log2 of their sums, a flag
 constexpr int kAtOnce = 8;             // log sums of a row that are fetched together
 constexpr float kTiny = 1e-38f;        // a factor of 0 would turn a masked -inf into NaN
@@ -638,7 +639,9 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                                     // (a row that sees any key of a tile sees its first)
                                     if (m_run == kNegInf)
                                         m_run = x[0] * fb[0];
-                                    const float nm = decltype(masked)::value && m_run == kNegInf ? 0.f : -m_run;
+                                    // without any score yet: hidden keys are 0 against the largest float,
+                                    // and a score (the first was -inf) is infinite, which sums the tile again
+                                    const float nm = decltype(masked)::value && m_run == kNegInf ? kMost : -m_run;
                                     const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
                                     for (int e = 0; e < 16; e += 2) {

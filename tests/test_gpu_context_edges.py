@@ -96,3 +96,92 @@ def test_weights_whose_sums_run_out_leave_the_totals_alone(cache):
     run_weights(b, 0.09, 64, w, **kw)
     assert int(b.err.item()) == 0
     weights_close(w, before.double().cpu().numpy()[..., :add.shape[2]], add, size, "after a time-out")
+
+
+# ------------------------------------------------------------------ infinities in 16-bit caches
+
+INFINITIES = [
+    # heads, kv, D, bs, new, cached, window, keys of score -inf, keys of score +inf
+    (1, 1, 64, 16, [1], [4], 1, [0], []),
+    (4, 2, 64, 8, [3, 5], [40, 7], 2, [0], []),
+    (4, 4, 128, 16, [20], [130], 20, [0, 16, 128], []),
+    (8, 1, 128, 32, [40], [300], 33, list(range(17)), []),     # 264 rows; a whole column block, and one more
+    (2, 2, 64, 16, [9], [380], 8, list(range(130)) + [256], []),       # a whole tile
+    (2, 1, 64, 16, [1], [129], 1, list(range(128)), []),       # all but the last two
+    (4, 2, 64, 16, [30], [110], 30, [0, 128], [135]),          # rows from 135 on see +inf
+    (2, 2, 128, 16, [4], [400], 3, [5], [128]),                # every row does
+    (2, 1, 64, 8, [20], [0], 6, [1, 3], [16]),
+    (1, 1, 64, 16, [2], [20000], 2, [0, 128, 2560], []),       # an item over every CTA
+    # warps of 32 rows each (a row of nobody is zeros, and 0 times an infinity NaN)
+    (32, 1, 64, 16, [1], [4], 1, [0], []),                     # five tokens: no column behind the first 16
+    (4, 4, 64, 8, [32], [5], 32, [0], []),
+    (8, 1, 128, 16, [16], [120], 16, [0, 16, 128], []),        # where tiles and column blocks start
+    (16, 1, 64, 16, [8], [250], 8, list(range(128, 145)), []), # an edge tile behind an inner one
+    (16, 1, 128, 32, [48], [240], 48, [256], [270]),           # 768 rows; those from 270 on see +inf
+    (32, 1, 64, 16, [1], [130], 1, list(range(129)), []),      # a tile of which the rows see two keys
+]
+
+
+@pytest.mark.parametrize("dt", [W.F16, W.BF16])
+@pytest.mark.parametrize("i", range(len(INFINITIES)))
+def test_weights_of_keys_with_infinite_scores(i, dt):
+    """-inf is a weight of 0, and the others keep theirs; a row that sees +inf is NaN
+    where it sees a key, and reaches no other."""
+    h, kv, d, bs, new, cached, window, low, high = INFINITIES[i]
+    b, gk, desc, k = sixteen_bit(440 + i, dt, h, kv, d, bs, new, cached)
+    b.q[..., 0] = 0.25 + np.abs(b.q[..., 0])
+    b.q = b.dev16(b.q).double().cpu().numpy()
+    finite = k.copy()
+    for keys, value in ((low, -np.inf), (high, np.inf)):
+        for s, c in enumerate(b.ctx):
+            for t in keys:
+                if t < c:
+                    k[b.tables[s, t // bs], :, t % bs, 0] = value
+                    finite[b.tables[s, t // bs], :, t % bs, 0] = 0.0
+    gk.copy_(torch.from_numpy(k))
+    w = torch.zeros(len(new), kv, b.max_ctx, device="cuda")
+    run_weights(b, 0.125, window, w, desc=desc)
+    assert int(b.err.item()) == 0
+    _, size = OC.weights(Keys(b, k=finite), b.q, b.cu, window, b.ctx, 0.125)
+    with np.errstate(invalid="ignore"):
+        add, _ = OC.weights(Keys(b, k=k), b.q, b.cu, window, b.ctx, 0.125)
+    nan = np.isnan(add)
+    assert nan.any() == bool(high) and np.array_equal(w.isnan().cpu().numpy(), nan)
+    weights_close(w.nan_to_num(0.0), 0.0, np.nan_to_num(add), size, "infinite scores")
+
+
+@pytest.mark.parametrize("dt", [W.F16, W.BF16])
+def test_weights_nan_in_a_sixteen_bit_cache(dt):
+    """A NaN key makes the rows that see it NaN where they see a key; behind a row's
+    position, behind a context or in a block of nobody it reaches nothing."""
+    b, gk, desc, k = sixteen_bit(460, dt, 4, 2, 64, 16, [12, 3], [190, 40])
+    used = np.unique(np.concatenate([b.tables[s, :-(-c // 16)] for s, c in enumerate(b.ctx)]))
+    k[np.setdiff1d(np.arange(b.nb), used)] = np.nan
+    for s, c in enumerate(b.ctx):                             # slots behind the last token
+        k[b.tables[s, (c - 1) // 16], :, c % 16 or 16:] = np.nan
+    k[b.tables[0, 195 // 16], 1, 195 % 16, 7] = np.nan        # rows at 195 and later see it
+    gk.copy_(torch.from_numpy(k))
+    w = torch.zeros(2, 2, b.max_ctx, device="cuda")
+    run_weights(b, 0.125, 12, w, desc=desc)
+    assert int(b.err.item()) == 0
+    got = w.isnan().cpu().numpy()
+    want = np.zeros_like(got)
+    want[0, 1, :202] = True
+    assert np.array_equal(got, want)
+    add, size = OC.weights(Keys(b, k=np.nan_to_num(k)), b.q, b.cu, 12, b.ctx, 0.125)
+    add[0, 1, :202] = 0
+    weights_close(w.nan_to_num(0.0), 0.0, add, size, "others")
+
+
+@pytest.mark.parametrize("dt", [W.F16, W.BF16])
+def test_weights_of_bad_blocks_in_a_sixteen_bit_cache(dt):
+    """Their keys are zeros, and get the weight of such a key."""
+    b, gk, desc, k = sixteen_bit(461, dt, 4, 2, 64, 8, [9, 4], [150, 5])
+    for (s, j), bad in {(0, 0): -1, (0, 16): b.nb, (0, 17): 1 << 30, (1, 1): b.nb + 7}.items():
+        k[b.tables[s, j]] = 0.0
+        b.gt[s, j] = bad
+    w = torch.zeros(2, 2, b.max_ctx, device="cuda")
+    run_weights(b, 0.125, 5, w, desc=desc)
+    assert int(b.err.item()) == B.PKV_DEVERR_BLOCK_ID
+    add, size = OC.weights(Keys(b, k=k), b.q, b.cu, 5, b.ctx, 0.125)
+    weights_close(w, 0.0, add, size, "bad blocks")
