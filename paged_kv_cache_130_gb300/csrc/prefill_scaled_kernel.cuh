@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     __shared__ uint32_t ref_bits[2];           // largest ks, vs of the CTA's blocks
-    __shared__ int any_rest;                   // some scale is no power of two
-    __shared__ float rests[NR][2][NB];         // then: the rests of ks, vs by tile
+    __shared__ int any_rest;                   // some scale is no power of two (PREFIX: or a block is bad)
+    __shared__ float rests[NR][2][NB];         // then: the rests of ks, vs by tile (PREFIX: bad blocks' ks 0)
     __shared__ int nan_pos[D];                 // first key whose V is NaN in this column
     __shared__ int any_nan;
     __shared__ int64_t first_rows[2];          // where the query tiles' outputs start
@@ -401,12 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_holder;
     auto block_ok = [&](int phys) { return phys >= 0 && (int64_t)phys < p.num_blocks; };
+    // (PREFIX: the keys of such a block are masked by the form with rests)
+    auto bad_block = [&]() {
+        flag_error(p.dev_err, PKV_DEVERR_BLOCK_ID);
+        if constexpr (PREFIX)
+            *reinterpret_cast<volatile int*>(&any_rest) = 1;
+    };
     float2 sc_first = make_float2(0.f, 0.f);
     if (tid < nblocks) {
         if (block_ok(id_first))
             sc_first = __ldg(scales + (int64_t)id_first * p.num_kv_heads + g);
         else
-            flag_error(p.dev_err, PKV_DEVERR_BLOCK_ID);
+            bad_block();
     }
     // ---------------- what can start before the scales are known ----------------
     // Softmax warps: q, in its own type.  A warp copies its 32 rows side by side
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = tid + kThreads; b < nblocks; b += kThreads) {
             const int phys = __ldg(table + b);
             if (!block_ok(phys)) {
-                flag_error(p.dev_err, PKV_DEVERR_BLOCK_ID);
+                bad_block();
                 continue;
             }
             const float2 sc = __ldg(scales + (int64_t)phys * p.num_kv_heads + g);
@@ -628,7 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float f = rest[b];
 #pragma unroll
                         for (int j = 0; j < BS; ++j)
-                            x[b * BS + j] *= f;
+                            if constexpr (PREFIX)
+                                x[b * BS + j] = f == 0.f ? kNegInf : x[b * BS + j] * f;
+                            else
+                                x[b * BS + j] *= f;
                     }
                 }
                 // row max: eight independent chains of three-input maxima
@@ -663,7 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 m_run = m_new;
                 const float2 qk2 = make_float2(qk, qk);
-                const float2 nm2 = make_float2(kWeightExp - m_new, kWeightExp - m_new);
+                // (PREFIX: no key of the tiles so far is there: -inf + 0 is no weight)
+                const float nm = PREFIX && kRests && m_new == kNegInf ? 0.f : kWeightExp - m_new;
+                const float2 nm2 = make_float2(nm, nm);
                 float2 ls[4] = {};                     // four pairs of partial sums
                 // P over S: 16 keys as 8 columns of fp16 pairs at the start of
                 // those keys' own 16 columns
@@ -915,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             const uint32_t dst = sb + L::slot + st * L::SLOT;
             if (uneven && j < nk && cw == 0 && lane < NB) {
-                rests[j & (NR - 1)][0][lane] = rest_of(sc0.x);
+                rests[j & (NR - 1)][0][lane] = PREFIX && !block_ok(id0) ? 0.f : rest_of(sc0.x);
                 rests[j & (NR - 1)][1][lane] = rest_of(sc0.y);
             }
             // each place is refilled for the next slot once its codes are used

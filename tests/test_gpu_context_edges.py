@@ -8,9 +8,10 @@ import torch
 
 import harness as H
 from oracle import context as OC
+from oracle import scaled as OS
 from paged_kv_cache_130_gb300 import binding as B
 from paged_kv_cache_130_gb300 import workloads as W
-from test_gpu_context import Keys, run_weights, weights_close
+from test_gpu_context import Keys, Shared, run_weights, weights_close
 from test_gpu_scaled import TD, Batch
 
 pytestmark = pytest.mark.gpu
@@ -185,3 +186,44 @@ def test_weights_of_bad_blocks_in_a_sixteen_bit_cache(dt):
     assert int(b.err.item()) == B.PKV_DEVERR_BLOCK_ID
     add, size = OC.weights(Keys(b, k=k), b.q, b.cu, 5, b.ctx, 0.125)
     weights_close(w, 0.0, add, size, "bad blocks")
+
+
+# ------------------------------------------------------------------ shared prefixes
+
+BAD_BLOCKS = [
+    # dtype, heads, kv, D, bs, members, prefix blocks, their own tokens, bad blocks of the prefix
+    (W.F16, 4, 2, 64, 16, 3, 10, [20, 1, 7], [0, 4]),                        # shares, 6 rows
+    (W.BF16, 8, 1, 128, 16, 4, 10, [20, 1, 7, 0], [9]),                      # shares, 32 rows
+    (W.BF16, 8, 1, 128, 16, 5, 10, [20, 1, 7, 0, 3], [9]),                   # the kernel of the prefixes, 40
+    (W.F16, 16, 2, 64, 16, 9, 70, [3] * 9, list(range(32, 64))),             # a run of bad blocks only
+    (W.BF16, 8, 2, 128, 8, 12, 140, [1, 30] * 6, list(range(16)) + [40, 139]),   # first a tile of them
+    (W.F16, 8, 1, 64, 32, 6, 40, [2] * 6, list(range(0, 40, 2))),
+    (W.BF16, 3, 1, 128, 16, 20, 6, [5, 70] * 10, list(range(6))),            # all of them
+    (W.F16, 3, 1, 128, 16, 2, 6, [5, 70], list(range(6))),
+    (W.F16, 4, 4, 64, 16, 40, 9, [4] * 40, [3]),
+]
+
+
+@pytest.mark.parametrize("odd_scales", [False, True])
+@pytest.mark.parametrize("i", range(len(BAD_BLOCKS)))
+def test_bad_blocks_of_a_shared_prefix_contribute_nothing(i, odd_scales):
+    """On either side of the rule that gives prefixes a kernel of their own, as in the
+    plain decode: the attention over the tokens that are there."""
+    dt, h, kv, d, bs, members, blocks, own, bad = BAD_BLOCKS[i]
+    b = Shared(470 + i, dt, h, kv, d, bs, [(blocks, own), (2, [9, 1])])
+    if odd_scales:
+        b.scales *= np.random.default_rng(i).uniform(1, 2, b.scales.shape).astype(np.float32)
+        b.gs.copy_(torch.from_numpy(b.scales))
+    for n, j in enumerate(bad):
+        b.gt[:members, j] = (-1, b.nb, 1 << 30)[n % 3]
+    out = b.shared(0.125)
+    assert int(b.err.item()) == B.PKV_DEVERR_BLOCK_ID
+    # the reference: tables without those blocks
+    stay = [j for j in range(b.tables.shape[1]) if j not in bad]
+    tables = b.tables.copy()
+    tables[:members] = -1
+    tables[:members, :len(stay)] = b.tables[:members][:, stay]
+    ctx = b.ctx.copy()
+    ctx[:members] -= bs * len(bad)
+    ref = OS.attention(b.k, b.v, b.scales, b.q, b.cu, tables, ctx, 0.125)
+    H.assert_attention_close(out.double().cpu().numpy(), ref, "bad prefix blocks", dt)
