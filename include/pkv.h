@@ -682,6 +682,8 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
  * cache, scales  scales NULL: a 16-bit cache with q of the same type, or an E4M3
  *                cache with k_scale; otherwise a scaled cache, whose scales are
  *                positive, normal and finite.  V is not read.
+ * window         min(window, max_context_len) times the query heads of a KV head is
+ *                2^30 at most (else PKV_ERR_UNSUPPORTED, and a workspace of 0).
  * q              device [total_q][num_heads][head_dim], F16 or BF16, 1..128 query
  *                heads per KV head (a cache of E4M3 codes takes bf16 rows as fp16
  *                times a power of two: elements below 2^-28 of the row's largest

@@ -732,8 +732,9 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                                    : 1.f;
                             // (uniform) some row does not see some key of the tile
                             const bool edge = (w.j0 + j) * kRows + kRows - 1 > w.first_pos;
-                            // the first row that sees the key, of the q tile's
-                            const int lo = (key - w.first_pos) * p.group - row0 - qt * kRows;
+                            // the first row that sees the key, of the q tile's (keys in front of
+                            // the rows may be further off than 32 bits hold times the heads)
+                            const int lo = max(key - w.first_pos, 0) * p.group - row0 - qt * kRows;
                             const float f = fmaxf(k_scale * info[0], kTiny);
                             const float2 f2 = make_float2(f, f);
                             if (even && !edge && end == kRows) {

@@ -143,6 +143,12 @@ WeightsLayout weights_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t 
     return w;
 }
 
+// (row, query head) rows of a KV head: a sequence has no more rows than its context.
+int64_t window_rows(const pkv_cache_desc* c, int32_t num_heads, int32_t window, int32_t max_context_len)
+{
+    return (int64_t)(window < max_context_len ? window : max_context_len) * (num_heads / c->num_kv_heads);
+}
+
 // The weights of a window: launches of up to kWindowSeqs sequences, which share the
 // scratch.
 struct WindowLayout {
@@ -155,10 +161,8 @@ WindowLayout window_layout(const pkv_cache_desc* c, int32_t num_seqs, int32_t nu
                            int32_t max_context_len)
 {
     WindowLayout w{};
-    // (a sequence has no more rows than its context)
-    const int64_t rows = window < max_context_len ? window : max_context_len;
     w.seqs = num_seqs < pkv::kWindowSeqs ? num_seqs : pkv::kWindowSeqs;
-    w.row_tiles = (int32_t)((rows * (num_heads / c->num_kv_heads) + 127) / 128);
+    w.row_tiles = (int32_t)((window_rows(c, num_heads, window, max_context_len) + 127) / 128);
     w.ctas = device_sms();
     const int64_t tiles = (int64_t)w.seqs * c->num_kv_heads * w.row_tiles;
     w.info_off = tiles * 128 * c->head_dim * 2;
@@ -236,7 +240,8 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
 size_t pkv_attention_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
                                              int32_t num_heads, int32_t window, int32_t max_context_len)
 {
-    if (!sizes_known(cache, num_seqs, num_heads, max_context_len) || window <= 0)
+    if (!sizes_known(cache, num_seqs, num_heads, max_context_len) || window <= 0 ||
+        window_rows(cache, num_heads, window, max_context_len) > pkv::kWindowRows)
         return 0;
     return (size_t)window_layout(cache, num_seqs, num_heads, window, max_context_len).bytes;
 }
@@ -259,6 +264,7 @@ pkv_status pkv_attention_weights(const pkv_cache_desc* cache, const float* scale
         !lengths_ok(max_blocks_per_seq, max_context_len, cache->block_size))
         return PKV_ERR_INVALID_ARG;
     if (num_heads / cache->num_kv_heads > 128 ||
+        window_rows(cache, num_heads, window, max_context_len) > pkv::kWindowRows ||
         (cache->cache_dtype != PKV_FP8_E4M3 && cache->cache_dtype != q_dtype))
         return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || total_q == 0 || window == 0 || max_context_len == 0)

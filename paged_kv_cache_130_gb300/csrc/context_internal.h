@@ -9,6 +9,7 @@
 namespace pkv {
 
 constexpr int kWindowSeqs = 512;       // sequences a launch of attention weights takes
+constexpr int64_t kWindowRows = 1 << 30;   // (row, query head) rows of a KV head that its 32 bits hold
 
 struct WeightsParams {
     const void* k_cache;

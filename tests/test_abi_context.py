@@ -229,3 +229,14 @@ def test_binding_checks():
                      d, s, q, t, c, 10, c[:2], c[:1], 3, 1, 0.1)):
         with pytest.raises(ValueError, match="must be on the current CUDA device"):
             call()
+
+
+def test_windows_of_more_rows_than_32_bits_hold(lib):
+    """min(window, max_context_len) x query heads of a KV head beyond 2^30."""
+    d = _desc(num_kv_heads=1)
+    a = dict(WEIGHTS, heads=128, window=(1 << 23) + 1, maxc=1 << 30, ws=None)
+    assert lib.pkv_attention_weights(ctypes.byref(d), *a.values()) == UNSUPPORTED
+    assert B.pkv_attention_weights_workspace_bytes(d, 2, 128, a["window"], a["maxc"]) == 0
+    a = dict(a, maxc=1 << 23, seq=1 << 23, head=1 << 23)              # (no more rows than a context has)
+    assert lib.pkv_attention_weights(ctypes.byref(d), *a.values()) == WORKSPACE
+    assert B.pkv_attention_weights_workspace_bytes(d, 2, 128, a["window"], a["maxc"]) > 1 << 37

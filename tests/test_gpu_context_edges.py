@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import harness as H
+import oracle
 from oracle import context as OC
 from oracle import scaled as OS
 from paged_kv_cache_130_gb300 import binding as B
@@ -227,3 +228,38 @@ def test_bad_blocks_of_a_shared_prefix_contribute_nothing(i, odd_scales):
     ctx[:members] -= bs * len(bad)
     ref = OS.attention(b.k, b.v, b.scales, b.q, b.cu, tables, ctx, 0.125)
     H.assert_attention_close(out.double().cpu().numpy(), ref, "bad prefix blocks", dt)
+
+
+# ------------------------------------------------------------------ lengths whose products pass 32 bits
+
+@pytest.mark.parametrize("heads,ctx,size", [
+    (128, (1 << 24) + 500, 20),                 # a power of two for each row of q
+    (100, (1 << 31) // 100 + 700, 0),           # rows that do not fill a tile
+])
+def test_weights_of_keys_far_behind_the_window(heads, ctx, size):
+    """Millions of tokens of a few blocks, one row of many heads: tokens x heads passes
+    32 bits for the first ones."""
+    r = np.random.default_rng(7)
+    kinds, d, bs = 128, 64, 32
+    k = r.integers(0, 256, (4, 1, bs, d), dtype=np.uint8) & 0xb7       # (at most 0.9375)
+    q = r.standard_normal((1, heads, d))
+    q[0, heads // 2] *= 2.0 ** -size
+    gq = torch.from_numpy(q).bfloat16().cuda()
+    gk = torch.from_numpy(k).cuda()
+    gv = torch.zeros_like(gk)
+    gs = torch.ones(4, 1, 2, device="cuda")
+    table = (torch.arange(-(-ctx // bs), dtype=torch.int32, device="cuda") % 4).view(1, -1)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.zeros(1, 1, ctx, device="cuda")
+    lens = torch.tensor([ctx], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    B.pkv_attention_weights(B.cache_desc(gk, gv), gq, cu, 1, table, lens, ctx, 0.25, w, scales=gs, dev_err=err)
+    assert int(err.item()) == 0
+    x = gq[0].double().cpu().numpy()
+    keys = oracle.decode(oracle.E4M3, k).reshape(kinds, d)
+    s = 0.25 * x @ keys.T
+    p = np.exp(s - s.max(1, keepdims=True))
+    counts = np.full(kinds, ctx // kinds) + (np.arange(kinds) < ctx % kinds)
+    add = (p / (p * counts).sum(1, keepdims=True)).sum(0)
+    add = np.tile(add, -(-ctx // kinds))[None, None, :ctx]
+    weights_close(w, 0.0, add, 0.25 * (abs(x) @ abs(keys).T).max(), "far")
