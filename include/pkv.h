@@ -686,8 +686,8 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
  *                2^30 at most (else PKV_ERR_UNSUPPORTED, and a workspace of 0).
  * q              device [total_q][num_heads][head_dim], F16 or BF16, 1..128 query
  *                heads per KV head (a cache of E4M3 codes takes bf16 rows as fp16
- *                times a power of two: elements below 2^-28 of the row's largest
- *                may be rounded).
+ *                times a power of two: elements below 2^-18 of the row's largest
+ *                may be off by up to 2^-26 of it).
  * workspace      pkv_attention_weights_workspace_bytes bytes, 256-byte aligned.
  * Device checks as for the prefill: a sequence that cannot be used gets nothing
  * added; a key of a block with a bad id is read as zeros.  PKV_DEVERR_TIMEOUT: where a

@@ -117,8 +117,11 @@ constexpr float kSpread = 4096.f;      // rows of a tile within it share a power
 
 // One CTA = one tile of 128 rows; D / 8 lanes to a row.  QT: type of q, CT: of the
 // operand.  Where they differ, rows are scaled by a power of two: the one of the tile's
-// largest element, if no row's largest is further than kSpread below it (a row's
-// elements are then off by 2^-27 of its largest at most), else each row's own.
+// largest element, if no row's largest is further than kSpread below it, else each
+// row's own.  The tile's largest then lies in [2^13, 2^14) and a row's at 2 or above,
+// where fp16's step is 2^-24 at least: bf16's 8 bits fit from 2^-18 of the row's largest
+// on, smaller elements are off by 2^-26 of it at most.  (Rows with factors of their own:
+// 2^-30 and 2^-38.)
 template <int QT, int CT, int D>
 __global__ void __launch_bounds__(kTileThreads) weights_tiles_kernel(const WeightsParams p)
 {

@@ -263,3 +263,39 @@ def test_weights_of_keys_far_behind_the_window(heads, ctx, size):
     add = (p / (p * counts).sum(1, keepdims=True)).sum(0)
     add = np.tile(add, -(-ctx // kinds))[None, None, :ctx]
     weights_close(w, 0.0, add, 0.25 * (abs(x) @ abs(keys).T).max(), "far")
+
+
+# ------------------------------------------------------------------ rows of very different size
+
+@pytest.mark.parametrize("exact", [True, False])
+def test_weights_of_small_elements_beside_a_large_one(exact):
+    """bf16 rows of a tile share a power of two while their largest elements lie within
+    2^12 of each other: a row's elements from 2^-18 of its largest on are exact, smaller
+    ones off by 2^-26 of it at most.  Here a row's large element meets keys of 0, and the
+    small ones decide."""
+    b = Batch(480, W.BF16, 4, 2, 64, 16, [20], [300])
+    b.append()
+    b.oracle_append()
+    b.k[..., 0] = 0
+    b.gk.copy_(torch.from_numpy(b.k))
+    r = np.random.default_rng(1)
+    low = -18 if exact else -24
+    q = r.choice([-1.0, 1.0], b.q.shape) * (1 + r.integers(0, 128, b.q.shape) / 128) * \
+        2.0 ** r.integers(low, -15 if exact else -20, b.q.shape)
+    q[..., 0] = 1.0                             # (the row's largest: up to 2^-12 of the tile's)
+    q[7, 1, 0] = 2.0 ** 12
+    b.q = q
+    assert np.array_equal(b.dev16(q).double().cpu().numpy(), q)
+    scale = 2.0 ** (12 if exact else 17)
+    w = torch.zeros(1, 2, b.max_ctx, device="cuda")
+    run_weights(b, scale, 20, w, scales=b.gs)
+    assert int(b.err.item()) == 0
+    keys = Keys(b)
+    add, size = OC.weights(keys, b.q, b.cu, 20, b.ctx, scale)
+    if not exact:
+        # what the elements lose moves a score by 2^-26 of the row's largest times the
+        # key's magnitudes; the bound of a score is 2^-19 (size + 1)
+        lost = scale * 2.0 ** -26 * max(np.abs(keys(0, h)).sum(1).max() for h in range(2))
+        assert lost < 0.2
+        size += lost * 2.0 ** 19
+    weights_close(w, 0.0, add, size, "small elements")
