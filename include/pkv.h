@@ -663,7 +663,7 @@ pkv_status pkv_paged_attention_decode_scaled_shared_prefix(
  * context:
  *   weights  device float, entry (s, g, t) at s * weights_seq + g * weights_head + t
  *            (strides in elements; rows hold max_context_len entries at least and do
- *            not overlap).
+ *            not overlap, the heads of a sequence side by side or the sequences of a head).
  * pkv_attention_weights adds the weights of a prompt's last rows (or of all),
  * pkv_paged_attention_decode_scaled_weights those of a decode step; both add to
  * what is there, so a new sequence's row starts at zero.  pkv_evict keeps the

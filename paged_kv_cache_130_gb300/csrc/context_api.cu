@@ -28,11 +28,19 @@ bool sizes_known(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_heads, i
            max_context_len <= INT_MAX - 1024;
 }
 
-// Rows of at least `len` entries that do not overlap (null where there are none).
+// n runs of m rows each of at least `len` entries, the runs `outer` apart and their rows
+// `inner`, do not overlap.
+bool rows_apart(int64_t outer, int64_t n, int64_t inner, int64_t m, int64_t len)
+{
+    return (m <= 1 || inner >= len) && (n <= 1 || (outer >= len && (m <= 1 || inner <= (outer - len) / (m - 1))));
+}
+
+// Rows of at least `len` entries that do not overlap, sequence by sequence or head by
+// head (null where there are none).
 bool weights_ok(const float* w, int64_t seq, int64_t head, int32_t num_seqs, int32_t heads, int64_t len)
 {
-    return (w != nullptr || len == 0) && aligned(w, 4) && (heads <= 1 || head >= len) &&
-           (num_seqs <= 1 || seq >= (heads - 1) * head + len);
+    return (w != nullptr || len == 0) && aligned(w, 4) &&
+           (rows_apart(seq, num_seqs, head, heads, len) || rows_apart(head, heads, seq, num_seqs, len));
 }
 
 // Two arrays of n entries that have none in common.

@@ -240,3 +240,25 @@ def test_windows_of_more_rows_than_32_bits_hold(lib):
     a = dict(a, maxc=1 << 23, seq=1 << 23, head=1 << 23)              # (no more rows than a context has)
     assert lib.pkv_attention_weights(ctypes.byref(d), *a.values()) == WORKSPACE
     assert B.pkv_attention_weights_workspace_bytes(d, 2, 128, a["window"], a["maxc"]) > 1 << 37
+
+
+@pytest.mark.parametrize("seq,head,want", [
+    (1000, 2000, WORKSPACE),                                   # head by head (the next check's answer)
+    (1500, 2500, WORKSPACE),
+    (8000, 1000, WORKSPACE),
+    (1000, 1999, INVALID),
+    (999, 5000, INVALID),
+    (1000, 1000, INVALID),
+    (-1000, 2000, INVALID),
+    (1 << 62, 1 << 62, INVALID),                               # (the same row, modulo 2^64 in bytes)
+    (1 << 62, 1 << 60, INVALID),
+])
+def test_totals_of_either_order(lib, seq, head, want):
+    """Two sequences, eight heads, rows of 1,000."""
+    for fn, args in ((lib.pkv_attention_weights, WEIGHTS),
+                     (lib.pkv_paged_attention_decode_scaled_weights, dict(DECODE, seqs=2)),
+                     (lib.pkv_evict, EVICT)):
+        a = dict(args, seq=seq, head=head, ws=None)
+        assert fn(ctypes.byref(_desc()), *a.values()) == want
+    a = dict(EVICT, wo_seq=seq, wo_head=head, ws=None)
+    assert lib.pkv_evict(ctypes.byref(_desc()), *a.values()) == want

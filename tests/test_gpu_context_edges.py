@@ -12,7 +12,7 @@ from oracle import context as OC
 from oracle import scaled as OS
 from paged_kv_cache_130_gb300 import binding as B
 from paged_kv_cache_130_gb300 import workloads as W
-from test_gpu_context import Keys, Shared, run_weights, weights_close
+from test_gpu_context import Evicted, Keys, Shared, run_weights, weights_close
 from test_gpu_scaled import TD, Batch
 
 pytestmark = pytest.mark.gpu
@@ -299,3 +299,33 @@ def test_weights_of_small_elements_beside_a_large_one(exact):
         assert lost < 0.2
         size += lost * 2.0 ** 19
     weights_close(w, 0.0, add, size, "small elements")
+
+
+# ------------------------------------------------------------------ totals in any order
+
+def by_head(n, kv, tokens):
+    """Totals [n, kv, tokens] that lie head by head."""
+    return torch.rand(kv, n, tokens, device="cuda").transpose(0, 1)
+
+
+def test_totals_that_lie_head_by_head():
+    """Rows that do not overlap, the KV heads outside the sequences."""
+    b = Batch(490, W.F16, 4, 2, 64, 16, [5, 1, 9], [100, 40, 3])
+    b.append()
+    b.oracle_append()
+    w = by_head(3, 2, b.max_ctx + 1)
+    assert w.stride(1) > w.stride(0) > b.max_ctx
+    dense = w.contiguous()
+    run_weights(b, 0.125, 4, w, scales=b.gs)
+    run_weights(b, 0.125, 4, dense, scales=b.gs)
+    assert torch.equal(w, dense)
+    one = Batch(491, W.F16, 4, 2, 64, 16, [1, 1, 1], [100, 40, 3])
+    one.append()
+    args = (one.desc, one.gs, one.dev16(one.q), one.gt, one.gctx, one.max_ctx, 0.125)
+    for t in (w, dense):
+        B.pkv_paged_attention_decode_scaled_weights(*args, t, dev_err=one.err)
+    assert torch.equal(w, dense)
+    e = Evicted(492, "scaled", 64, 16, 2, [100, 37, 5], [40, 37, 50], 4, 8)
+    lens, out = e.run(weights_out=by_head(3, 2, e.max_ctx + 2))
+    e.check(lens, out)
+    assert int(b.err.item()) == int(one.err.item()) == int(e.err.item()) == 0
