@@ -47,6 +47,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "context_internal.h"
@@ -1167,7 +1168,7 @@ template <int QT, int CT, bool E8, int D>
 cudaError_t run(const WeightsParams& p, cudaStream_t stream)
 {
     using L = Layout<D, E8>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];      // (threads may call at once)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)

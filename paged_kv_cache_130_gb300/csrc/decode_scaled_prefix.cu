@@ -18,6 +18,8 @@
 // and their own tokens in one softmax: 81 and 75.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "decode_scaled_kernel.cuh"
 #include "prefill_scaled_kernel.cuh"
 
@@ -78,7 +80,7 @@ cudaError_t run_prefixes(const DecodeParams& p, const float* scales, int64_t fir
 {
     using L = pfs::Layout<D>;
     auto kern = pfs::prefill_scaled_kernel<QT, D, BS, true>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];      // (threads may call at once)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -145,7 +147,7 @@ cudaError_t run(const DecodeParams& p0, const float* scales, int32_t* first, int
     DecodeExtra x{};
     x.first = first;
     auto kern = decode_scaled_kernel<QT, D, BS, NNT, true, kShared>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];      // (threads may call at once)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)

@@ -1,6 +1,8 @@
 // prefill_scaled.cu -- causal attention over a scaled cache: launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "prefill_scaled_kernel.cuh"
 
 namespace pkv {
@@ -14,7 +16,7 @@ cudaError_t run(const ScaledPrefillParams& sp, cudaStream_t stream)
     using L = Layout<D>;
     const PrefillParams& p = sp.p;
     auto kern = prefill_scaled_kernel<QT, D, BS, false>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];      // (threads may call at once)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)

@@ -40,6 +40,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "tc_common.cuh"
@@ -572,7 +574,7 @@ cudaError_t run_prefill_ws(const PrefillParams& p, cudaStream_t stream)
 {
     using L = WsLayout<D>;
     auto kern = prefill_ws_kernel<CT, D, BS>;
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];      // (threads may call at once)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)

@@ -2,6 +2,8 @@
 run out, infinities and NaN in 16-bit caches, blocks that cannot be used, rows of
 very different size, lengths whose products pass 32 bits.  Bounds as in
 test_gpu_context."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -329,3 +331,49 @@ def test_totals_that_lie_head_by_head():
     lens, out = e.run(weights_out=by_head(3, 2, e.max_ctx + 2))
     e.check(lens, out)
     assert int(b.err.item()) == int(one.err.item()) == int(e.err.item()) == 0
+
+
+# ------------------------------------------------------------------ calls at once
+
+def test_calls_of_several_threads_at_once():
+    """Four threads, each on a stream and with tensors of its own, make every call again
+    and again: the results are those of one call after the other."""
+    jobs = []
+    for i in range(4):
+        s = Shared(500 + i, W.F16, 8, 2, 64, 16, [(40, [3] * 10), (0, [5])])     # 40 rows: both kernels
+        b, kw, _ = weighed(W.BF16 if i % 2 else "scaled", [40, 1], [500 + i, 129])
+        n = torch.zeros(2, 2, b.max_ctx, device="cuda")
+        e = Evicted(510 + i, torch.float16, 64, 16, 2, [700, 301], [256, 128], 4, 64)
+        t = torch.zeros(11, 2, s.max_ctx, device="cuda")
+
+        def work(s=s, b=b, kw=kw, n=n, e=e, t=t):
+            a = s.shared(0.125)
+            run_weights(b, 0.09, 16, n.zero_(), **kw)
+            B.pkv_paged_attention_decode_scaled_weights(s.desc, s.gs, s.dev16(s.q), s.gt, s.gctx, s.max_ctx,
+                                                        0.125, t.zero_(), dev_err=s.err)
+            return [a, n.clone(), t.clone()] + list(e.run())
+
+        want = work()
+        torch.cuda.synchronize()
+        jobs.append((work, want, s, b, e))
+    wrong, start = [], threading.Barrier(4)
+
+    def go(i):
+        try:
+            work, want = jobs[i][:2]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait(30)
+                for _ in range(20):
+                    got = work()
+                    torch.cuda.current_stream().synchronize()
+                    wrong.extend(i for x, y in zip(got, want) if not torch.equal(x, y))
+        except Exception as ex:                      # (a thread's own failure is the test's)
+            wrong.append(ex)
+
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not wrong
+    assert all(int(x.err.item()) == 0 for j in jobs for x in j[2:])
