@@ -377,3 +377,113 @@ def test_calls_of_several_threads_at_once():
         x.join()
     assert not wrong
     assert all(int(x.err.item()) == 0 for j in jobs for x in j[2:])
+
+
+# ------------------------------------------------------------------ evictions with bad blocks
+
+@pytest.mark.parametrize("cache", ["scaled", "e4m3", torch.bfloat16])
+def test_evict_with_bad_blocks_and_unusable_sequences_in_full(cache):
+    """Every byte of the pools, the scales, totals and lengths: the usable sequence and
+    the good blocks are as without the others, what a bad block holds or would hold is
+    left out, and nothing else changes."""
+    e = Evicted(520, cache, 64, 16, 2, [100, 50, 64, 40, 70], [40, 30, 33, 20, 20], 1, 2, odd_scales=True)
+    keep, ctx, tables, dst = e.keep.copy(), e.ctx.copy(), e.tables.copy(), e.dst.copy()
+    e.keep[1], e.ctx[3] = -1, e.max_ctx + 1
+    e.tables[2, 0], e.tables[2, 3] = -3, 1 << 20               # (its first token stays in any case)
+    e.dst[4, 1] = len(e.k)
+    out = torch.full(e.w.shape, 9.0, device="cuda")
+    lens, got = e.run(weights_out=out)
+    torch.cuda.synchronize()
+    assert int(e.err.item()) == B.PKV_DEVERR_CONTEXT | B.PKV_DEVERR_BLOCK_ID
+    assert lens.tolist() == [40, 0, 33, 0, 20]
+    k, v, sc = e.k.copy(), e.v.copy(), None if e.scales is None else e.scales.copy()
+    want = np.full(e.w.shape, 9.0, np.float32)
+    for s, n in ((0, 40), (2, 33), (4, 20)):
+        want[s] = 0
+        for h in range(2):
+            idx = OC.kept(e.w[s, h, :ctx[s]], n, 1, 2)
+            want[s, h, :n] = e.w[s, h, idx]
+            for b0 in range(0, n, 16):
+                part = idx[b0:b0 + 16]
+                slot = np.arange(len(part))
+                if (s, b0) == (4, 16):
+                    continue                                   # the destination that is not there
+                if s == 2:
+                    there = (part // 16 != 0) & (part // 16 != 3)
+                    part, slot = part[there], slot[there]
+                src, to = tables[s, part // 16], int(dst[s, b0 // 16])
+                for j, (pool, old) in enumerate(((k, e.k), (v, e.v))):
+                    x = old[src, h, part % 16]
+                    if sc is not None and len(part):
+                        was = e.scales[src, h, j]
+                        sc[to, h, j] = was.max()
+                        f = (was / was.max())[:, None]         # fp32, as its rounding
+                        y = (oracle.decode(oracle.E4M3, np.ascontiguousarray(x)).astype(np.float32) * f)
+                        x = np.where(f == 1, x, oracle.encode_e4m3(y.astype(np.float32)))
+                    pool[to, h, slot] = x
+    bits = torch.uint8 if e.k.dtype == np.uint8 else torch.int16
+    assert np.array_equal(e.gk.view(bits).cpu().numpy(), k) and np.array_equal(e.gv.view(bits).cpu().numpy(), v)
+    assert sc is None or np.array_equal(e.gs.cpu().numpy(), sc)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ prefixes with a kernel of their own
+
+def test_prefix_kernel_on_another_stream_in_graphs_and_twice_over_a_workspace():
+    """80 rows of a group over 1,600 tokens (runs of 512 keys): the shares' kernel starts
+    beside the prefixes' and waits at its end, and the reduce behind both.  Two batches
+    over one workspace, on a stream of their own and in graphs that are replayed in
+    turn, give the bits that each gives alone."""
+    pair = [Shared(530, W.BF16, 8, 1, 128, 16, [(100, [100, 3, 40, 1, 0, 9, 64, 65, 2, 500])]),
+            Shared(531, W.BF16, 8, 1, 128, 16, [(33, [7] * 8), (70, [1, 300])])]
+    calls, want = [], []
+    for b in pair:
+        n, groups = len(b.ctx), len(b.prefix)
+        size = int(np.diff(b.begin).max())
+        assert 8 * size > 32
+        calls.append(dict(cache=b.desc, scales=b.gs, q=b.dev16(b.q), block_tables=b.gt, context_lens=b.gctx,
+                          max_context_len=b.max_ctx, group_begin=torch.from_numpy(b.begin).cuda(),
+                          group_prefix_blocks=torch.from_numpy(b.prefix).cuda(), max_group_size=size,
+                          max_prefix_blocks=int(b.prefix.max()), scale=0.09, dev_err=b.err,
+                          out=torch.empty(n, 8, 128, dtype=torch.bfloat16, device="cuda")))
+        calls[-1]["need"] = B.pkv_decode_scaled_shared_prefix_workspace_bytes(b.desc, n, 8, groups, size, b.max_ctx)
+        want.append(b.shared(0.09))
+        H.assert_attention_close(want[-1].double().cpu().numpy(), b.attention(0.09), "prefix kernel", W.BF16)
+    ws = torch.empty(max(c.pop("need") for c in calls), dtype=torch.uint8, device="cuda")
+    fn = B.pkv_paged_attention_decode_scaled_shared_prefix
+    torch.cuda.synchronize()
+
+    def right():
+        torch.cuda.synchronize()
+        for c, x in zip(calls, want):
+            assert torch.equal(c["out"], x)
+            c["out"].zero_()
+        ws.fill_(0xff)                                        # (NaN wherever a partial is not written again)
+
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        for c in calls:
+            fn(**c, workspace=ws, stream=side)
+    right()
+    for _ in range(20):
+        for c in calls:
+            fn(**c, workspace=ws)
+    right()
+    graphs = []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fn(**c, workspace=ws)
+        graphs.append(g)
+    for _ in range(20):
+        for g in graphs:
+            g.replay()
+    right()
+    both = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(both):
+        for c in calls:
+            fn(**c, workspace=ws)
+    for _ in range(20):
+        both.replay()
+    right()
+    assert all(int(b.err.item()) == 0 for b in pair)
