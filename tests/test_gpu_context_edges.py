@@ -487,3 +487,26 @@ def test_prefix_kernel_on_another_stream_in_graphs_and_twice_over_a_workspace():
         both.replay()
     right()
     assert all(int(b.err.item()) == 0 for b in pair)
+
+
+# ------------------------------------------------------------------ a scale of 0
+
+def test_a_scale_of_zero_weighs_every_token_alike():
+    """Every call: the mean over the tokens, weights of 1 / their number."""
+    for members in (3, 10):                                    # 12 rows a group, and 40: shares, own kernel
+        s = Shared(540 + members, W.F16, 8, 2, 64, 16, [(40, [3] * members), (0, [5])])
+        H.assert_attention_close(s.shared(0.0).double().cpu().numpy(), s.attention(0.0), "scale 0", W.F16)
+        w = torch.zeros(members + 1, 2, s.max_ctx, device="cuda")
+        B.pkv_paged_attention_decode_scaled_weights(s.desc, s.gs, s.dev16(s.q), s.gt, s.gctx, s.max_ctx, 0.0, w,
+                                                    dev_err=s.err)
+        add, size = OC.weights(Keys(s), s.q, s.cu, 1, s.ctx, 0.0)
+        assert size == 0.0
+        weights_close(w, 0.0, add, size, "scale 0")
+        assert int(s.err.item()) == 0
+    for cache in ("scaled", W.F16, W.BF16):
+        b, kw, keys = weighed(cache, [40, 1], [300, 129])
+        w = torch.zeros(2, 2, b.max_ctx, device="cuda")
+        run_weights(b, 0.0, 33, w, **kw)
+        add, size = OC.weights(keys, b.q, b.cu, 33, b.ctx, 0.0)
+        weights_close(w, 0.0, add, size, "scale 0")
+        assert int(b.err.item()) == 0
