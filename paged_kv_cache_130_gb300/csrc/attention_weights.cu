@@ -32,7 +32,8 @@
 // finishes the item last merges them.  Every wait is bounded.
 //
 // Bound by the chain product - softmax - product through tensor memory, of which
-// two sets of 128 x 256 scores fit: ~2,600 cycles a key tile for 1,024 of products.
+// two sets of 128 x 256 scores fit: ~2,600 cycles a key tile for 1,024 of products and
+// 1,024 of exponentials (32,768 at 32 a cycle; both pipes are 36-38 % busy).
 // Measured: 32 rows of 4 prompts after 16,384..32,768 tokens (64 heads over 8, D
 // 128) 165 us; 64 rows of 8 prompts of 512..2,048 (32 heads, bf16 cache) 57 us.  On the
 // way: a CTA per run of keys with two groups of softmax warps 267 us, equal shares
@@ -41,8 +42,9 @@
 // Block ids asked for four tiles ahead instead of two: 169 and 55.6.  Few rows (5 of 6
 // prompts of 10,594..21,189 tokens, 16 heads each its own) take 160 us at 32 tokens a
 // block and 220 at 8: ~1,700 and ~2,400 cycles a tile, one bulk copy for each block of
-// it (two teams of converting warps changed nothing).  The merge fetches 8 log sums of a row at once: one by one the sums pass over 5 prompts
-// of 8,765..17,530 tokens of one head took 31 us instead of 20.
+// it (two teams of converting warps changed nothing).  The merge fetches 8 log sums of a
+// row at once: one by one the sums pass over 5 prompts of 8,765..17,530 tokens of one head
+// took 31 us instead of 20.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
