@@ -451,8 +451,13 @@ __global__ void __launch_bounds__((kNC + 1) * 32, 4)
             const bool ok = __all_sync(0xffffffffu,
                                        wait_or_abort(full0 + 8 * stage, (tt / NSTG) & 1,
                                                      abort_flag, p.dev_err, tries));
+            // After a tile that did not come no other is looked at: while a stage's copy
+            // is on its way, the phase of its next use reads as the one before, complete;
+            // freeing the stage then lets the producer start a second copy in one phase.
+            if (!ok)
+                break;
             const int4 md = meta[stage];
-            if (ok && ((md.x >> 16) & 1)) {
+            if ((md.x >> 16) & 1) {
                 const int rlo = md.x & 0xff;
                 const int rhi = (md.x >> 8) & 0xff;
                 const int t_end = md.z;
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__((kNC + 1) * 32, 4)
                 }
             }
             __syncwarp();
-            if (ok && lane == 0)
+            if (lane == 0)
                 tc::bar_arrive(empty0 + 8 * stage);
         }
 
