@@ -562,9 +562,11 @@ __global__ void __launch_bounds__((NC + 1) * 32, 3)
             // so a slow reader of item n never sees item n+1's value)
             if (warp == 0) {
                 const int qs = n % kItemQueue;
+                // (no item after one that some warp gave up on, see its tiles below)
                 const bool ok = __all_sync(
-                    0xffffffffu, wait_bounded(&iq_full[qs], (n / kItemQueue) & 1, abort_flag,
-                                              p.dev_err, tries));
+                                    0xffffffffu, wait_bounded(&iq_full[qs], (n / kItemQueue) & 1,
+                                                              abort_flag, p.dev_err, tries)) &&
+                                !*abort_flag;
                 const int item = ok ? items[qs] : -1;
                 __syncwarp();
                 if (lane == 0)
@@ -618,14 +620,20 @@ __global__ void __launch_bounds__((NC + 1) * 32, 3)
                     const bool ok = __all_sync(
                         0xffffffffu, wait_bounded(&full[stage], (tt / NSTG) & 1, abort_flag,
                                                   p.dev_err, tries));
-                    if (ok && flags[stage]) {
+                    // After a tile that did not come no other is looked at: while a
+                    // stage's copies are on their way, the phase of its next use reads as
+                    // the one before, complete; freeing the stage then lets the producer
+                    // start more copies in one phase.
+                    if (!ok)
+                        break;
+                    if (flags[stage]) {
                         const char* sk =
                             reinterpret_cast<const char*>(ring + stage * Shape::STAGE);
                         st.consume(sk, sk + Shape::VOFF, qf, lane, w.t_begin + k * BS + tsub,
                                    w.t_end);
                     }
                     __syncwarp();
-                    if (ok && lane == 0)
+                    if (lane == 0)
                         mbar_arrive(&empty[stage]);
                 }
                 // filed by block residue k0, not by warp: the merge then adds the
