@@ -949,6 +949,9 @@ __global__ void __launch_bounds__(threads_of<E8>(), 1)
                 const uint32_t slot = qn & 1;
                 if (qn >= 2 && !wait_one(s_addr(&bars.q_free[slot]), ((qn >> 1) & 1) ^ 1, waits))
                     return false;
+                // (a warp that gave up frees slots whose copy may be on its way: no second one)
+                if (aborted(&abort_flag))
+                    return false;
                 const uint32_t bar = s_addr(&bars.q_full[slot]);
                 expect_bytes(bar, L::TB + kInfo * 4);
 #pragma unroll
